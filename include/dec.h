@@ -470,6 +470,114 @@ enum { DEC_I8_PATH_DP4A = 0, DEC_I8_PATH_TCGEN05 = 1 };
 dec_status dec_i8_dot(const int8_t* xq, const int8_t* wq, int32_t m, int32_t n, int32_t kdim, int32_t path,
                       int32_t* acc, void* stream);
 
+/*
+ * Row-batch operators: a batch of streams, each owning some consecutive rows of the caller's
+ * row buffers, over a K/V cache in caller memory. One description serves the rows' storing
+ * (dec_kv4_write), their reading back (dec_kv4_read) and the attention of their queries
+ * (dec_attention_kv4, dec_attention_window), so one token per stream and ragged prompt chunks
+ * are the same calls. (Interface additions without a counterpart in the pages.)
+ *
+ * dec_kv_view: the cache. A pool of n_pages pages, each [n_kv_heads][page_rows] rows of 64 dims.
+ *   n_kv_heads      K/V heads
+ *   page_rows       rows per page: 16, 32 or 64; an f32 cache without a table may have any
+ *                   page_rows >= 1 when pages_per_slot is 1 (dec_attention's [batch, heads, ld,
+ *                   64] caches are page_rows = ld, pages_per_slot = 1)
+ *   pages_per_slot  logical pages of one slot; a slot holds page_rows * pages_per_slot rows
+ *   n_slots         slots
+ *   n_pages         pages in the pool
+ *   table           device int32 [n_slots, pages_per_slot], the physical page of each logical
+ *                   page; NULL: page p of slot s is s * pages_per_slot + p (n_pages must hold
+ *                   n_slots * pages_per_slot). Slots may share pages that are only read. An
+ *                   entry outside [0, n_pages) is a page without rows: its keys are not
+ *                   visible, rows are not stored there and read back as zeros.
+ *
+ * dec_kv_rows: the batch. Stream b owns rows row_start[b] .. row_start[b + 1] - 1 of the row
+ * buffers; with n of them they sit at positions lens[b] - n .. lens[b] - 1 of cache slot
+ * slots[b]. (lens counts the stream's rows: store them, then attend.)
+ *   batch      streams, 1..65535
+ *   n_rows     rows in the row buffers, >= 1
+ *   max_rows   upper bound on one stream's rows, 1..n_rows; a stream's rows beyond it are not
+ *              processed
+ *   row_start  device int32 [batch + 1], not decreasing, within [0, n_rows]; NULL: one row per
+ *              stream (row b; n_rows >= batch, max_rows 1). Rows of the buffers that belong to
+ *              no stream are left as they were.
+ *   slots      device int32 [batch], or NULL: 0..batch-1. dec_kv4_write needs distinct slots
+ *              (two streams storing the same row leave either one's values, or a mix). A slot
+ *              outside [0, n_slots) has no rows.
+ *   lens       device int32 [batch]. Positions below 0 or beyond the slot's rows are not
+ *              stored and read back as zeros; a query below position 0 gives zeros.
+ * The structs are host memory, read during the call; the device arrays are read by the queued
+ * kernels. The calls need no handle, allocate nothing, run on the calling thread's current
+ * device, do not synchronise, and can be captured into CUDA graphs. Errors set
+ * dec_last_error(NULL).
+ */
+typedef struct dec_kv_view {
+    int32_t n_kv_heads;
+    int32_t page_rows;
+    int32_t pages_per_slot;
+    int32_t n_slots;
+    int32_t n_pages;
+    const int32_t* table;
+} dec_kv_view;
+
+typedef struct dec_kv_rows {
+    int32_t batch;
+    int32_t n_rows;
+    int32_t max_rows;
+    const int32_t* row_start;
+    const int32_t* slots;
+    const int32_t* lens;
+} dec_kv_rows;
+
+/*
+ * Bytes of a 4-bit cache pool (K and V) for `view`: 72 per (row, K/V head) instead of f32's 512;
+ * 0 for a bad view. Each (page, head) block holds page_rows rows of K codes (32 bytes each:
+ * dim i in byte i / 2, low nibble first, code + 8), page_rows K scales (two bf16 each: dims
+ * 0..31 and 32..63), then the V codes and V scales alike.
+ * Codes: per (row, head, group of 32 dims) a = max |x|, s = a / 7 rounded to f32 and then to bf16
+ * (0 when below 2^-126), c = x / s rounded to the nearest integer, ties to even (decided exactly,
+ * not on a rounded quotient); the cache stands for c s, within s / 2 of x. A group with a NaN or
+ * an infinity reads back as NaN.
+ */
+size_t dec_kv4_bytes(const dec_kv_view* view);
+
+/*
+ * Quantise and store the batch's K and V rows: k and v device f32 [n_rows] rows of
+ * n_kv_heads * 64 (token-major, K already rotated), `ld` floats apart (ld >= n_kv_heads * 64, a
+ * multiple of 4, so rows inside a fused q|k|v buffer are taken in place); k, v and cache 16-byte
+ * aligned. cache: device, dec_kv4_bytes(view) bytes.
+ */
+dec_status dec_kv4_write(const dec_kv_view* view, const dec_kv_rows* rows, const float* k, const float* v, int64_t ld,
+                         void* cache, void* stream);
+
+/* Read the batch's rows back as f32 into k_out and v_out (device, the layout of dec_kv4_write). */
+dec_status dec_kv4_read(const dec_kv_view* view, const dec_kv_rows* rows, const void* cache, float* k_out,
+                        float* v_out, int64_t ld, void* stream);
+
+/*
+ * Attention of the batch's query rows over a 4-bit cache (dec_attention_kv4) or f32 caches
+ * (dec_attention_window: k and v device f32 pools of the view's pages, [n_pages, n_kv_heads,
+ * page_rows, 64]). A query at position p sees the keys j <= p of its slot with j > p - window
+ * (window 0: no limit) or j < sinks (the first tokens, which stay visible). For each head h, with
+ * the K/V head h / (n_heads / n_kv_heads): s_j = q . k_j / 8, max-subtracted softmax in f32,
+ * out = sum_j p_j v_j. A row that sees no key, or whose softmax sum is not finite and positive,
+ * gives zeros, as in dec_attention. Values of keys a query does not see never reach it, whatever
+ * they are (NaN, infinities, rows never written).
+ *   q, out    device f32 [n_rows] rows of n_heads * 64, q_ld and out_ld floats apart (multiples of 4)
+ *   n_heads   a multiple of n_kv_heads
+ *   workspace device scratch of dec_attention_rows_workspace_size(view, rows, n_heads) bytes. Its
+ *             contents need not be initialised and nothing is kept in it between calls; calls (or
+ *             graph replays) that may overlap on the GPU need one each.
+ * q, out, cache, k, v and workspace are 16-byte aligned.
+ */
+size_t dec_attention_rows_workspace_size(const dec_kv_view* view, const dec_kv_rows* rows, int32_t n_heads);
+dec_status dec_attention_kv4(const dec_kv_view* view, const dec_kv_rows* rows, const float* q, int64_t q_ld,
+                             int32_t n_heads, const void* cache, int32_t window, int32_t sinks, float* out,
+                             int64_t out_ld, void* workspace, size_t workspace_bytes, void* stream);
+dec_status dec_attention_window(const dec_kv_view* view, const dec_kv_rows* rows, const float* q, int64_t q_ld,
+                                int32_t n_heads, const float* k, const float* v, int32_t window, int32_t sinks,
+                                float* out, int64_t out_ld, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,84 @@
+// Host-only check of the row batch's index arithmetic (csrc/kv_rows.cuh): whatever the device
+// arrays hold, every place that kv_place returns lies inside the pool, rows lie inside the row
+// buffers, and well-formed batches get exactly their rows. Prints "ok".
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+
+#include "kv_rows.cuh"
+
+void dec_set_thread_error(const char*) {}
+
+using namespace dec;
+
+#define CHECK(c)                                             \
+    do {                                                     \
+        if (!(c)) {                                          \
+            std::printf("line %d: %s\n", __LINE__, #c);      \
+            return 1;                                        \
+        }                                                    \
+    } while (0)
+
+static unsigned seed = 12345;
+static unsigned rnd() { return seed = seed * 1664525u + 1013904223u; }
+static int wild() {
+    static const int v[] = {0, 1, -1, 5, 31, 32, 63, 64, 1000, -1000, 0x7fffffff, -0x7fffffff - 1, 0x7ffffff0};
+    return v[(rnd() >> 8) % (sizeof(v) / sizeof(v[0]))];
+}
+
+int main() {
+    const int shapes[][4] = {{16, 3, 4, 12}, {32, 1, 1, 1}, {64, 7, 5, 40}, {300, 1, 6, 6}, {16, 130000, 900, 5}};
+    for (const auto& sh : shapes) {
+        for (int paged = 0; paged < 2; ++paged) {
+            dec_kv_view v{3, sh[0], sh[1], sh[2], sh[3], nullptr};
+            if (sh[0] == 300 && paged) continue;
+            if (!paged) v.n_pages = v.n_slots * v.pages_per_slot;
+            std::vector<int> table(static_cast<size_t>(v.n_slots) * v.pages_per_slot);
+            for (auto& t : table) t = (rnd() >> 9) % 3 ? static_cast<int>((rnd() >> 4) % v.n_pages) : wild();
+            if (paged) v.table = table.data();
+            CHECK(view_problem(&v, false) == nullptr);
+            const KvViewDev d = view_dev(v);
+            const long long pool = static_cast<long long>(v.n_pages) * 3 * v.page_rows;
+            for (int rep = 0; rep < 4000; ++rep) {
+                const int B = 3, n_rows = 9;
+                int start[4], slots[3], lens[3];
+                for (int& x : start) x = (rnd() >> 9) % 2 ? static_cast<int>((rnd() >> 5) % 10) : wild();
+                for (int& x : slots) x = (rnd() >> 9) % 2 ? static_cast<int>((rnd() >> 5) % v.n_slots) : wild();
+                for (int& x : lens) x = (rnd() >> 9) % 2 ? static_cast<int>((rnd() >> 5) % 70) : wild();
+                dec_kv_rows r{B, n_rows, 1 + static_cast<int>((rnd() >> 6) % n_rows), rep % 5 ? start : nullptr,
+                              rep % 3 ? slots : nullptr, lens};
+                if (!r.row_start) r.max_rows = 1;
+                CHECK(rows_problem(&r) == nullptr);
+                const KvRowsDev rd = rows_dev(r);
+                for (int b = 0; b < B; ++b) {
+                    const StreamRows s = stream_rows(rd, d, b);
+                    CHECK(s.n >= 0 && s.n <= r.max_rows);
+                    CHECK(s.n == 0 || (s.row0 >= 0 && s.row0 + s.n <= n_rows));
+                    CHECK(s.slot >= -1 && s.slot < v.n_slots);
+                    for (int i = 0; i < s.n; ++i) {
+                        int page = -5, pr = -5;
+                        if (!kv_place(d, s, i, page, pr)) continue;
+                        CHECK(page >= 0 && page < v.n_pages && pr >= 0 && pr < v.page_rows);
+                        for (int h = 0; h < 3; ++h) {
+                            CHECK(kvf_block(d, page, h) / kHeadDim + pr < pool);
+                            CHECK(kv4_block(d, page, h) + static_cast<long long>(v.page_rows) * 72 <= pool * 72);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    // a well-formed ragged batch: stream 1 holds rows 2..5 at positions 29..32 of slot 2
+    const int start[] = {0, 2, 6, 6}, slots[] = {0, 2, 1}, lens[] = {2, 33, 0};
+    dec_kv_view v{2, 16, 3, 3, 9, nullptr};
+    dec_kv_rows r{3, 8, 4, start, slots, lens};
+    const KvViewDev d = view_dev(v);
+    const StreamRows s = stream_rows(rows_dev(r), d, 1);
+    CHECK(s.row0 == 2 && s.n == 4 && s.slot == 2 && s.pos0 == 29);
+    int page, pr;
+    CHECK(kv_place(d, s, 3, page, pr) && page == 2 * 3 + 2 && pr == 0);
+    CHECK(kv_place(d, s, 0, page, pr) && page == 2 * 3 + 1 && pr == 13);
+    CHECK(stream_rows(rows_dev(r), d, 2).n == 0);
+    std::printf("ok\n");
+    return 0;
+}

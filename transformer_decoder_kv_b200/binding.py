@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import sys
 from typing import Optional, Sequence
 
 import numpy as np
@@ -30,7 +31,8 @@ EXPORTS = ["dec_create", "dec_destroy", "dec_last_error", "dec_prefill", "dec_kv
            "dec_next_tokens", "dec_get_config", "dec_generate", "dec_set_prefill_chunk",
            "dec_set_phase_timing", "dec_phase_times", "dec_release_slot", "dec_kv_pages_free",
            "dec_attention_workspace_size", "dec_attention", "dec_attention_plan", "dec_attention_noalloc",
-           "dec_i8_dot"]
+           "dec_i8_dot", "dec_kv4_bytes", "dec_kv4_write", "dec_kv4_read",
+           "dec_attention_rows_workspace_size", "dec_attention_kv4", "dec_attention_window"]
 I8_PATH = {"dp4a": 0, "tcgen05": 1}
 DEC_INJECT_DROP_ATTN_COPY = 1
 PHASE_NAMES = {1: "embed", 2: "qkv", 3: "self_attn", 4: "o", 5: "cross_q", 6: "cross_attn", 7: "cross_o",
@@ -77,6 +79,16 @@ class DecWeights(C.Structure):
                 ("final_b", C.c_void_p), ("layers", C.POINTER(DecLayerWeights))]
 
 
+class DecKvView(C.Structure):
+    _fields_ = [("n_kv_heads", C.c_int32), ("page_rows", C.c_int32), ("pages_per_slot", C.c_int32),
+                ("n_slots", C.c_int32), ("n_pages", C.c_int32), ("table", C.c_void_p)]
+
+
+class DecKvRows(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("n_rows", C.c_int32), ("max_rows", C.c_int32), ("row_start", C.c_void_p),
+                ("slots", C.c_void_p), ("lens", C.c_void_p)]
+
+
 def load_library(path: str = LIB_PATH) -> C.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"CUDA decoder library not built: {path} is missing "
@@ -114,6 +126,13 @@ def load_library(path: str = LIB_PATH) -> C.CDLL:
         "dec_attention_plan": (C.c_int, [vp, i32, pi32]),
         "dec_attention_noalloc": (C.c_int, [vp, vp, vp, vp, i32, i32, i32, vp, vp]),
         "dec_i8_dot": (C.c_int, [vp, vp, i32, i32, i32, i32, vp, vp]),
+        "dec_kv4_bytes": (C.c_size_t, [vp]),
+        "dec_kv4_write": (C.c_int, [vp, vp, vp, vp, C.c_int64, vp, vp]),
+        "dec_kv4_read": (C.c_int, [vp, vp, vp, vp, vp, C.c_int64, vp]),
+        "dec_attention_rows_workspace_size": (C.c_size_t, [vp, vp, i32]),
+        "dec_attention_kv4": (C.c_int, [vp, vp, vp, C.c_int64, i32, vp, i32, i32, vp, C.c_int64, vp, C.c_size_t, vp]),
+        "dec_attention_window": (C.c_int, [vp, vp, vp, C.c_int64, i32, vp, vp, i32, i32, vp, C.c_int64, vp,
+                                           C.c_size_t, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -354,3 +373,158 @@ def attention_workspace_size(batch: int, n_heads: int, ld: int) -> int:
 
 def i8_dot(xq, wq, m: int, n: int, kdim: int, acc, stream: int = 0, path: str = "dp4a"):
     _raise_thread_error(lib().dec_i8_dot(_ptr(xq), _ptr(wq), m, n, kdim, I8_PATH[path], _ptr(acc), stream))
+
+
+# ---- row-batch operators: 4-bit caches and windowed attention ------------------------------------
+
+def _einval(msg: str):
+    raise DecError(DEC_EINVAL, msg)
+
+
+def _device_array(name: str, a, dtype: str, least: int, device=None) -> Optional[int]:
+    """Pointer of a contiguous device array of at least `least` elements of a type."""
+    if a is None:
+        return None
+    if hasattr(a, "data_ptr"):
+        if str(a.dtype) != "torch." + dtype:
+            _einval(f"{name}: expected {dtype}, got {a.dtype}")
+        if not a.is_contiguous():
+            _einval(f"{name}: must be contiguous")
+        if a.numel() < least:
+            _einval(f"{name}: {a.numel()} elements, needs {least}")
+        if not a.is_cuda or (device is not None and a.device != device):
+            _einval(f"{name}: must be on {device or 'a CUDA device'}, is on {a.device}")
+    return _ptr(a)
+
+
+def _row_buffer(name: str, a, n_rows: int, width: int, device=None):
+    """(pointer, floats between rows) of f32 rows: [n_rows, width] or [n_rows, heads, 64] with
+    contiguous rows, any row stride."""
+    if not hasattr(a, "data_ptr"):
+        return _ptr(a), width
+    if str(a.dtype) != "torch.float32":
+        _einval(f"{name}: expected float32, got {a.dtype}")
+    if not a.is_cuda or (device is not None and a.device != device):
+        _einval(f"{name}: must be on {device or 'a CUDA device'}, is on {a.device}")
+    shape, stride = a.shape, a.stride()
+    inner, expect = 1, 1
+    for n, st in zip(reversed(shape[1:]), reversed(stride[1:])):
+        if n != 1 and st != expect:
+            _einval(f"{name}: the values of a row must be contiguous")
+        expect *= n
+        inner *= n
+    if len(shape) < 2 or inner != width:
+        _einval(f"{name}: expected rows of {width} values, got shape {tuple(shape)}")
+    if shape[0] < n_rows:
+        _einval(f"{name}: {shape[0]} rows, needs {n_rows}")
+    return a.data_ptr(), stride[0] if shape[0] > 1 else width
+
+
+class KvView:
+    """A K/V cache in caller memory (dec_kv_view): n_slots slots of pages_per_slot pages of
+    page_rows rows and n_kv_heads heads, through an int32 page table on the device
+    ([n_slots, pages_per_slot], pages of a pool of n_pages) or, without one, slot by slot."""
+
+    def __init__(self, n_kv_heads: int, page_rows: int, pages_per_slot: int, n_slots: int, n_pages: int = 0,
+                 table=None):
+        self.table = table          # kept alive with the description
+        self.device = getattr(table, "device", None)
+        ptr = _device_array("table", table, "int32", n_slots * pages_per_slot)
+        self.c = DecKvView(n_kv_heads, page_rows, pages_per_slot, n_slots, n_pages or n_slots * pages_per_slot, ptr)
+        self.ref = C.byref(self.c)
+
+
+class KvRows:
+    """A row batch (dec_kv_rows): stream b owns rows row_start[b] .. row_start[b + 1] - 1 (one row per
+    stream without row_start) at the last positions of lens[b] in cache slot slots[b]. lens, slots
+    and row_start are int32 device arrays; they may be rewritten between calls (or replays)."""
+
+    def __init__(self, batch: int, lens, slots=None, row_start=None, n_rows: int = 0, max_rows: int = 1):
+        self.keep = (lens, slots, row_start)
+        self.device = getattr(lens, "device", None)
+        self.c = DecKvRows(batch, n_rows or batch, max_rows,
+                           _device_array("row_start", row_start, "int32", batch + 1, self.device),
+                           _device_array("slots", slots, "int32", batch, self.device),
+                           _device_array("lens", lens, "int32", batch))
+        self.n_rows = n_rows or batch
+        self.ref = C.byref(self.c)
+
+
+def _same_device(view: KvView, rows: KvRows):
+    """The page table and the batch are on one device, the one the kernels will run on."""
+    if view.device is not None and rows.device is not None and view.device != rows.device:
+        _einval(f"the page table is on {view.device}, the batch on {rows.device}")
+    if rows.device is not None:
+        torch = sys.modules.get("torch")
+        if torch is not None and rows.device.index != torch.cuda.current_device():
+            _einval(f"the batch is on {rows.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def kv4_bytes(view: KvView) -> int:
+    """Bytes of a 4-bit cache pool for `view`."""
+    n = int(lib().dec_kv4_bytes(view.ref))
+    if n == 0:
+        _einval("dec_kv4_bytes: bad view")
+    return n
+
+
+def kv4_write(view: KvView, rows: KvRows, k, v, cache, stream: int = 0):
+    """Quantise and store the batch's K and V rows (f32 [n_rows, n_kv_heads * 64], any row stride)."""
+    _kv4_rows("dec_kv4_write", view, rows, k, v, cache, stream)
+
+
+def kv4_read(view: KvView, rows: KvRows, cache, k_out, v_out, stream: int = 0):
+    """Read the batch's rows back as f32."""
+    _kv4_rows("dec_kv4_read", view, rows, k_out, v_out, cache, stream)
+
+
+def _kv4_rows(name: str, view: KvView, rows: KvRows, k, v, cache, stream: int):
+    _same_device(view, rows)
+    width = view.c.n_kv_heads * 64
+    kp, ld = _row_buffer("k", k, rows.n_rows, width, rows.device)
+    vp, ld_v = _row_buffer("v", v, rows.n_rows, width, rows.device)
+    if ld != ld_v:
+        _einval(f"{name}: k and v have different row strides")
+    cp = _device_array("cache", cache, "uint8", _lib_bytes(view), rows.device)
+    if name == "dec_kv4_write":
+        st = lib().dec_kv4_write(view.ref, rows.ref, kp, vp, ld, cp, stream)
+    else:
+        st = lib().dec_kv4_read(view.ref, rows.ref, cp, kp, vp, ld, stream)
+    _raise_thread_error(st)
+
+
+def _lib_bytes(view: KvView) -> int:
+    return int(lib().dec_kv4_bytes(view.ref))
+
+
+def attention_rows_workspace_size(view: KvView, rows: KvRows, n_heads: int) -> int:
+    """Scratch bytes of attention_kv4 / attention_window for these sizes."""
+    n = int(lib().dec_attention_rows_workspace_size(view.ref, rows.ref, n_heads))
+    if n == 0:
+        _einval("dec_attention_rows_workspace_size: bad view, rows or n_heads")
+    return n
+
+
+def attention_kv4(view: KvView, rows: KvRows, q, cache, n_heads: int, out, workspace, workspace_bytes: int,
+                  window: int = 0, sinks: int = 0, stream: int = 0):
+    """Attention of the batch's query rows (f32 [n_rows, n_heads * 64]) over a 4-bit cache: each sees
+    the keys up to its own position, the last `window` of them (0: all) and the first `sinks`."""
+    _same_device(view, rows)
+    qp, q_ld = _row_buffer("q", q, rows.n_rows, n_heads * 64, rows.device)
+    op, o_ld = _row_buffer("out", out, rows.n_rows, n_heads * 64, rows.device)
+    cp = _device_array("cache", cache, "uint8", _lib_bytes(view), rows.device)
+    _raise_thread_error(lib().dec_attention_kv4(view.ref, rows.ref, qp, q_ld, n_heads, cp, window, sinks, op, o_ld,
+                                                _ptr(workspace), workspace_bytes, stream))
+
+
+def attention_window(view: KvView, rows: KvRows, q, k, v, n_heads: int, out, workspace, workspace_bytes: int,
+                     window: int = 0, sinks: int = 0, stream: int = 0):
+    """attention_kv4 over f32 caches k and v ([n_pages, n_kv_heads, page_rows, 64] each)."""
+    _same_device(view, rows)
+    qp, q_ld = _row_buffer("q", q, rows.n_rows, n_heads * 64, rows.device)
+    op, o_ld = _row_buffer("out", out, rows.n_rows, n_heads * 64, rows.device)
+    least = view.c.n_pages * view.c.n_kv_heads * view.c.page_rows * 64
+    kp = _device_array("k", k, "float32", least, rows.device)
+    vp = _device_array("v", v, "float32", least, rows.device)
+    _raise_thread_error(lib().dec_attention_window(view.ref, rows.ref, qp, q_ld, n_heads, kp, vp, window, sinks, op,
+                                                   o_ld, _ptr(workspace), workspace_bytes, stream))

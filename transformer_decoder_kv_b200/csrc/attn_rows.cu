@@ -1,0 +1,149 @@
+// Attention of a row batch's queries with a sliding window and sinks, over a 4-bit cache
+// (dec_attention_kv4) or f32 caches (dec_attention_window).
+//
+// A query at position p sees key j iff j <= p and (window == 0 or j > p - window or j < sinks):
+// s_j = q . k_j / 8, p_j = exp(s_j - max), out = sum_j p_j v_j / sum_j p_j, zeros where the sum is
+// not finite and positive.
+//
+// One warp per (row, head), lane = two dims; one pass over the visible keys with the running
+// maximum and sum.
+#include "kv_rows.cuh"
+
+using namespace dec;
+
+namespace {
+
+struct RowsAttnArgs {
+    KvViewDev v;
+    KvRowsDev r;
+    const float* q;
+    long long q_ld;
+    int heads, group;            // query heads, query heads per K/V head
+    const unsigned char* cache;  // 4-bit pool, or
+    const float* k;              // f32 pools
+    const float* vv;
+    int window, sinks;
+    float* out;
+    long long out_ld;
+};
+
+template <bool KV4>
+__global__ void __launch_bounds__(128) k_attn_rows(const RowsAttnArgs a) {
+    const int lane = threadIdx.x & 31;
+    const StreamRows s = stream_rows(a.r, a.v, blockIdx.z);
+    const int i = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y;
+    if (i >= s.n) return;
+    const int hk = h / a.group;
+    const long long row = s.row0 + i;
+    const float2 q = *reinterpret_cast<const float2*>(a.q + row * a.q_ld + h * kHeadDim + 2 * lane);
+    const long long p = s.pos0 + i;
+    float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+    const long long end = s.slot < 0 ? 0 : min(p + 1, kv_capacity(a.v));
+    const long long lo = a.window > 0 ? max(0ll, p - a.window + 1) : 0;
+    long long j = a.sinks > 0 ? 0 : lo;
+    while (j < end) {
+        if (j < lo && j >= a.sinks) {
+            j = lo;
+            continue;
+        }
+        const int page = kv_page(a.v, s.slot, static_cast<int>(j) >> a.v.shift);
+        const int pr = a.v.shift == 31 ? static_cast<int>(j) : static_cast<int>(j) & (a.v.page_rows - 1);
+        ++j;
+        if (page < 0) continue;
+        float2 k, v;
+        if (KV4) {
+            const unsigned char* blk = a.cache + kv4_block(a.v, page, hk);
+            auto get = [&](const unsigned char* part) {
+                const int c = part[pr * 32 + lane];
+                const float sc = __uint_as_float(
+                    static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(part + a.v.page_rows * 32 + pr * 4 +
+                                                                             (lane >> 4) * 2)) << 16);
+                return make_float2(sc * static_cast<float>((c & 15) - 8), sc * static_cast<float>((c >> 4) - 8));
+            };
+            k = get(blk);
+            v = get(blk + a.v.page_rows * kKv4RowBytes);
+        } else {
+            const long long off = kvf_block(a.v, page, hk) + static_cast<long long>(pr) * kHeadDim + 2 * lane;
+            k = *reinterpret_cast<const float2*>(a.k + off);
+            v = *reinterpret_cast<const float2*>(a.vv + off);
+        }
+        const float sc = warp_sum(fmaf(q.x, k.x, q.y * k.y)) * 0.125f;
+        const float mn = fmaxf(m, sc);
+        const float corr = m == mn ? 1.0f : expf(m - mn);
+        const float w = sc == -INFINITY ? 0.0f : expf(sc - mn);
+        l = fmaf(l, corr, w);
+        if (w != 0.0f) {
+            o0 = fmaf(w, v.x, o0 * corr);
+            o1 = fmaf(w, v.y, o1 * corr);
+        }
+        m = mn;
+    }
+    const bool ok = l > 0.0f && isfinite(l);
+    *reinterpret_cast<float2*>(a.out + row * a.out_ld + h * kHeadDim + 2 * lane) =
+        ok ? make_float2(o0 / l, o1 / l) : make_float2(0.0f, 0.0f);
+}
+
+template <bool KV4>
+dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows* rows, const float* q, int64_t q_ld,
+                     int32_t n_heads, const void* cache, const float* k, const float* v, int32_t window,
+                     int32_t sinks, float* out, int64_t out_ld, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+    const char* bad = view_problem(view, KV4);
+    if (!bad) bad = rows_problem(rows);
+    if (!bad && (!q || !out || !workspace || (KV4 ? !cache : (!k || !v)))) bad = "null pointer";
+    if (!bad && (n_heads < 1 || n_heads > 65535 || n_heads % view->n_kv_heads))
+        bad = "n_heads must be a multiple of n_kv_heads, at most 65535";
+    if (!bad && (window < 0 || sinks < 0)) bad = "window and sinks must be >= 0";
+    const int64_t d = static_cast<int64_t>(n_heads) * kHeadDim;
+    if (!bad && (q_ld < d || out_ld < d || ((q_ld | out_ld) & 3)))
+        bad = "q_ld and out_ld must be multiples of 4 and at least n_heads * 64";
+    if (!bad && !(aligned16(q) && aligned16(out) && aligned16(workspace) && aligned16(cache) && aligned16(k) &&
+                  aligned16(v)))
+        bad = "q, out, workspace and the caches must be 16-byte aligned";
+    if (!bad && workspace_bytes < dec_attention_rows_workspace_size(view, rows, n_heads)) bad = "workspace too small";
+    if (bad) return rows_fail(who, DEC_EINVAL, bad);
+    RowsAttnArgs a{};
+    a.v = view_dev(*view);
+    a.r = rows_dev(*rows);
+    a.q = q;
+    a.q_ld = q_ld;
+    a.heads = n_heads;
+    a.group = n_heads / view->n_kv_heads;
+    a.cache = static_cast<const unsigned char*>(cache);
+    a.k = k;
+    a.vv = v;
+    a.window = window;
+    a.sinks = sinks;
+    a.out = out;
+    a.out_ld = out_ld;
+    k_attn_rows<KV4><<<dim3((rows->max_rows + 3) / 4, n_heads, rows->batch), 128, 0,
+                       static_cast<cudaStream_t>(stream)>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return rows_cuda_fail(who, e, "k_attn_rows launch");
+    return DEC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dec_attention_rows_workspace_size(const dec_kv_view* view, const dec_kv_rows* rows, int32_t n_heads) {
+    if (view_problem(view, false) || rows_problem(rows) || n_heads < 1 || n_heads % view->n_kv_heads) return 0;
+    return 256;
+}
+
+dec_status dec_attention_kv4(const dec_kv_view* view, const dec_kv_rows* rows, const float* q, int64_t q_ld,
+                             int32_t n_heads, const void* cache, int32_t window, int32_t sinks, float* out,
+                             int64_t out_ld, void* workspace, size_t workspace_bytes, void* stream) {
+    return attn_rows<true>("dec_attention_kv4", view, rows, q, q_ld, n_heads, cache, nullptr, nullptr, window, sinks,
+                           out, out_ld, workspace, workspace_bytes, stream);
+}
+
+dec_status dec_attention_window(const dec_kv_view* view, const dec_kv_rows* rows, const float* q, int64_t q_ld,
+                                int32_t n_heads, const float* k, const float* v, int32_t window, int32_t sinks,
+                                float* out, int64_t out_ld, void* workspace, size_t workspace_bytes, void* stream) {
+    return attn_rows<false>("dec_attention_window", view, rows, q, q_ld, n_heads, nullptr, k, v, window, sinks, out,
+                            out_ld, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

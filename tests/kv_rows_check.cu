@@ -5,7 +5,7 @@
 #include <cstdlib>
 #include <vector>
 
-#include "kv_rows.cuh"
+#include "attn_rows.cuh"
 
 void dec_set_thread_error(const char*) {}
 
@@ -26,7 +26,58 @@ static int wild() {
     return v[(rnd() >> 8) % (sizeof(v) / sizeof(v[0]))];
 }
 
+// A unit's chunks hold every key that one of its rows sees exactly once, end inside the slot, and
+// are shared out completely among the splits; the launch bound covers them.
+template <int UR, int CK>
+static int check_units() {
+    for (int rep = 0; rep < 3000; ++rep) {
+        const int page_rows = rep % 3 ? 16 << (rep % 3) : 16, pages = 1 + static_cast<int>((rnd() >> 8) % 40);
+        dec_kv_view v{1, page_rows, pages, 1, pages, nullptr};
+        RowsAttnArgs a{};
+        a.v = view_dev(v);
+        a.group = 1 + static_cast<int>((rnd() >> 8) % 9);
+        a.heads = a.group;
+        a.window = (rnd() >> 8) % 3 ? static_cast<int>((rnd() >> 8) % 300) : 0;
+        a.sinks = (rnd() >> 8) % 2 ? static_cast<int>((rnd() >> 8) % 90) : 0;
+        a.S = 1 + static_cast<int>((rnd() >> 8) % 9);
+        a.min_chunks = 1 + static_cast<int>((rnd() >> 8) % 5);
+        StreamRows s;
+        s.row0 = 0;
+        s.n = 1 + static_cast<int>((rnd() >> 8) % 70);
+        s.slot = 0;
+        const long long cap = kv_capacity(a.v);
+        s.pos0 = static_cast<long long>((rnd() >> 8) % (cap + 40)) - 30;
+        const int units = (s.n * a.group + UR - 1) / UR;
+        for (int unit = 0; unit <= units; ++unit) {
+            const UnitKeys k = unit_keys<UR, CK>(a, s, unit);
+            CHECK(unit < units ? k.n_u >= 1 && k.n_u <= UR : k.n_u == 0);
+            if (!k.n_u) continue;
+            CHECK(k.splits >= 1 && k.splits <= a.S && k.end <= cap && k.total >= 0);
+            CHECK(k.total <= rows_max_chunks(a.v, s.n, a.window, a.sinks, CK));
+            CHECK(split_begin(k, 0) == 0 && split_begin(k, k.splits) == k.total);
+            std::vector<int> seen(cap + CK, 0);
+            for (int sp = 0; sp < k.splits; ++sp)
+                for (int t = split_begin(k, sp); t < split_begin(k, sp + 1); ++t)
+                    for (int j = 0; j < CK; ++j) {
+                        const long long at = static_cast<long long>(unit_chunk(k, t)) * CK + j;
+                        CHECK(at >= 0 && at < cap + CK);
+                        seen[at] += 1;
+                    }
+            for (int u = k.u0; u < k.u0 + k.n_u; ++u) {
+                const long long p = s.pos0 + u / a.group;
+                for (long long j = 0; j < cap; ++j) {
+                    const bool vis = j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
+                    CHECK(!vis || (seen[j] == 1 && j < k.end));
+                    CHECK(seen[j] <= 1);
+                }
+            }
+        }
+    }
+    return 0;
+}
+
 int main() {
+    if (check_units<8, 32>() || check_units<16, 32>()) return 1;
     const int shapes[][4] = {{16, 3, 4, 12}, {32, 1, 1, 1}, {64, 7, 5, 40}, {300, 1, 6, 6}, {16, 130000, 900, 5}};
     for (const auto& sh : shapes) {
         for (int paged = 0; paged < 2; ++paged) {

@@ -1,31 +1,13 @@
-// Attention of a row batch's queries with a sliding window and sinks, over a 4-bit cache
-// (dec_attention_kv4) or f32 caches (dec_attention_window).
-//
-// A query at position p sees key j iff j <= p and (window == 0 or j > p - window or j < sinks):
-// s_j = q . k_j / 8, p_j = exp(s_j - max), out = sum_j p_j v_j / sum_j p_j, zeros where the sum is
-// not finite and positive.
-//
-// One warp per (row, head), lane = two dims; one pass over the visible keys with the running
-// maximum and sum.
-#include "kv_rows.cuh"
+// dec_attention_kv4 and dec_attention_window: argument checks, the choice of kernel and split, and
+// the launches (kernels: attn_rows.cuh, attn_kv4_few.cuh).
+#include <algorithm>
+
+#include "attn_kv4_few.cuh"
+#include "attn_rows.cuh"
 
 using namespace dec;
 
 namespace {
-
-struct RowsAttnArgs {
-    KvViewDev v;
-    KvRowsDev r;
-    const float* q;
-    long long q_ld;
-    int heads, group;            // query heads, query heads per K/V head
-    const unsigned char* cache;  // 4-bit pool, or
-    const float* k;              // f32 pools
-    const float* vv;
-    int window, sinks;
-    float* out;
-    long long out_ld;
-};
 
 template <bool KV4>
 __global__ void __launch_bounds__(128) k_attn_rows(const RowsAttnArgs a) {
@@ -83,6 +65,49 @@ __global__ void __launch_bounds__(128) k_attn_rows(const RowsAttnArgs a) {
         ok ? make_float2(o0 / l, o1 / l) : make_float2(0.0f, 0.0f);
 }
 
+// Launch shape of a batch: unit rows per block, splits per unit.
+struct RowsPlan {
+    int unit_rows, tiles, S, min_chunks;
+};
+
+RowsPlan rows_plan(const dec_kv_view& view, const dec_kv_rows& rows, int n_heads, int window, int sinks) {
+    RowsPlan p;
+    const int group = n_heads / view.n_kv_heads;
+    const long long u = static_cast<long long>(rows.max_rows) * group;
+    p.unit_rows = u <= 8 ? 8 : 16;
+    p.tiles = static_cast<int>((u + p.unit_rows - 1) / p.unit_rows);
+    const long long units = static_cast<long long>(rows.batch) * view.n_kv_heads * p.tiles;
+    const long long chunks = rows_max_chunks(view_dev(view), rows.max_rows, window, sinks, kFewChunk);
+    p.min_chunks = kFewWarps;
+    const long long want = (8ll * kRowsSms + units - 1) / units, most = chunks / p.min_chunks;
+    p.S = static_cast<int>(std::max(1ll, std::min({want, most, static_cast<long long>(kRowsMaxSplits)})));
+    return p;
+}
+
+template <typename K, typename... Args>
+cudaError_t launch_after(K kern, dim3 grid, dim3 block, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int NT>
+cudaError_t launch_kv4_few(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
+    static_assert(kFewWarps * kFewStages * kFewStageBytes <= 48 * 1024, "no opt-in needed");
+    k_attn_kv4_few<NT><<<dim3(p.S, a.v.heads * p.tiles, a.r.batch), kFewWarps * 32, few_smem_bytes(NT), st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.S == 1) return e;
+    return launch_after(k_attn_merge<8 * NT, kFewChunk>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), dim3(128), st,
+                        a);
+}
+
 template <bool KV4>
 dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows* rows, const float* q, int64_t q_ld,
                      int32_t n_heads, const void* cache, const float* k, const float* v, int32_t window,
@@ -100,6 +125,8 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     if (!bad && !(aligned16(q) && aligned16(out) && aligned16(workspace) && aligned16(cache) && aligned16(k) &&
                   aligned16(v)))
         bad = "q, out, workspace and the caches must be 16-byte aligned";
+    if (!bad && (static_cast<long long>(rows->max_rows) * n_heads + 8 * view->n_kv_heads) / 8 > 65535)
+        bad = "max_rows * n_heads is too large";
     if (!bad && workspace_bytes < dec_attention_rows_workspace_size(view, rows, n_heads)) bad = "workspace too small";
     if (bad) return rows_fail(who, DEC_EINVAL, bad);
     RowsAttnArgs a{};
@@ -116,6 +143,15 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     a.sinks = sinks;
     a.out = out;
     a.out_ld = out_ld;
+    const RowsPlan plan = rows_plan(*view, *rows, n_heads, window, sinks);
+    a.part = static_cast<float*>(workspace);
+    a.S = plan.S;
+    a.min_chunks = plan.min_chunks;
+    if (KV4) {
+        const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        const cudaError_t e = plan.unit_rows == 8 ? launch_kv4_few<1>(a, plan, st) : launch_kv4_few<2>(a, plan, st);
+        return e == cudaSuccess ? DEC_OK : rows_cuda_fail(who, e, "k_attn_kv4_few launch");
+    }
     k_attn_rows<KV4><<<dim3((rows->max_rows + 3) / 4, n_heads, rows->batch), 128, 0,
                        static_cast<cudaStream_t>(stream)>>>(a);
     const cudaError_t e = cudaGetLastError();
@@ -129,7 +165,8 @@ extern "C" {
 
 size_t dec_attention_rows_workspace_size(const dec_kv_view* view, const dec_kv_rows* rows, int32_t n_heads) {
     if (view_problem(view, false) || rows_problem(rows) || n_heads < 1 || n_heads % view->n_kv_heads) return 0;
-    return 256;
+    const RowsPlan p = rows_plan(*view, *rows, n_heads, 0, 0);
+    return 256 + (p.S > 1 ? static_cast<size_t>(rows->n_rows) * n_heads * p.S * kPartStride * sizeof(float) : 0);
 }
 
 dec_status dec_attention_kv4(const dec_kv_view* view, const dec_kv_rows* rows, const float* q, int64_t q_ld,

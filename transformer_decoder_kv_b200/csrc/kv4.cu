@@ -51,7 +51,10 @@ __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const 
         float4* x = reinterpret_cast<float4*>((which ? vv : k) + static_cast<long long>(s.row0 + i) * ld +
                                               head * kHeadDim + l8 * 8);
         unsigned char* part = blk + which * v.page_rows * kKv4RowBytes;
-        uint32_t* codes = reinterpret_cast<uint32_t*>(part + pr * 32 + l8 * 4);
+        // K words sit in the order 0 4 1 5 2 6 3 7, so that one 8-byte load of the attention kernels
+        // gives 8 dims of each scale's group
+        const int word = which ? l8 : (l8 & 3) * 2 + (l8 >> 2);
+        uint32_t* codes = reinterpret_cast<uint32_t*>(part + pr * 32 + word * 4);
         uint16_t* scale = reinterpret_cast<uint16_t*>(part + v.page_rows * 32 + pr * 4 + (l8 >> 2) * 2);
         if (WRITE) {
             const float4 x0 = x[0], x1 = x[1];

@@ -1,29 +1,37 @@
 // Attention over a 4-bit cache for units of few query rows (decoding tokens, and the heads of a
-// group that share a K/V head): k_attn_kv4_few<NT>, up to 8 NT unit rows.
+// group that share a K/V head): k_attn_kv4_few<NT, PAIR>, up to 8 NT unit rows (4 with PAIR).
 //
-// Bound by the cache's 72 bytes per key, so the work per key must stay small: the codes go to the
-// tensor cores (mma.sync m16n8k16, f16) as the integers they are. tcgen05 would need the codes
-// unpacked into shared memory for tiles of 128 rows; here 1 to 16 rows meet each key once, and the
-// unpacked codes stay in the registers of the warp that read them.
+// The cache's 72 bytes per key are little beside the instructions a key takes, so those are what is
+// saved. The codes go to the tensor cores (mma.sync m16n8k16, f16) as the integers they are;
+// tcgen05 would need them unpacked into shared memory for tiles of 128 rows, and here 1 to 16 rows
+// meet each key once.
 //
-//   S^T = K Q^T   A = 16 keys x 64 dims (codes, exact in f16), B = 64 dims x 8 unit rows. Q is scaled
-//                 by a power of two per row and split into f16 high and low parts (22 bits), the two
-//                 products accumulate in f32, one accumulator per group of 32 dims, and the key's
-//                 two scales and the row's factor are applied to them in f32.
+//   S^T = K Q^T   A = 16 keys x 64 dims, B = 64 dims x 8 columns. A nibble masked out of its word and
+//                 read as f16 bits is n 2^-24 (or 16 n 2^-24), a subnormal number that the tensor
+//                 cores take exactly: no conversion. Q is scaled by a power of two per row and split
+//                 into an integer of up to 2048 and a remainder of at most 1 / 2, both in f16 (together
+//                 within 2^-23 of the row's largest element; dims met as 16 n are divided by 16).
+//                 The code is n - 8, so sum(q n) - 8 sum(q) is wanted: of the integer parts that is exact
+//                 in f32 (below 2^20 for the 32 dims of a group) and the accumulators just start at
+//                 -8 sum; the remainders' correction is added with the row's factor. One accumulator per
+//                 group; the key's two scales and the row's factor are applied in f32.
 //   softmax       running maximum per unit row and warp, p = exp2(s - m + 12), f32 sums.
 //   O^T += V^T P^T  A = 64 dims x 16 keys: code times scale, 3 + 8 significant bits, exact in f16
 //                 after the warp's power of two 2^-E (E follows the largest scale met so far);
-//                 B = p in f16 high and low parts. Each chunk of 32 keys sums into fresh
+//                 B = p in f16 high and low parts. Each chunk of 64 keys sums into fresh
 //                 accumulators that are added to the running f32 sums by ordinary fma, so that the
 //                 tensor cores' truncation does not build up over a long cache.
+//
+// With up to 4 unit rows (PAIR) columns 2 r and 2 r + 1 are row r's high and low parts: half the
+// products and half the softmax of the general form, where both parts take a product of their own.
 //
 // Fragment layouts decide the rest. Row r of S^T's 8-row halves is key (r >> 1) + 4 (r & 1), so that
 // after a transposing movmatrix a thread holds P^T's keys t, t + 4 (t + 8, t + 12) of its quad lane t, and
 // V's words of those keys are read without bank conflicts. A V word holds 8 dims of one key; two prmt
 // of the words of keys t and t + 4 give pairs along the keys, as the A fragment wants them.
 //
-// A warp owns every fourth chunk of 32 keys of the block's range and copies it into its own ring of
-// shared memory with cp.async, kStages - 1 chunks ahead; warps meet only at the end.
+// A warp owns every fourth chunk of 64 keys of the block's range and copies it into its own ring of
+// shared memory with cp.async, one chunk ahead; warps meet only at the end.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -32,9 +40,9 @@
 
 namespace dec {
 
-constexpr int kFewChunk = 32;
+constexpr int kFewChunk = 64;
 constexpr int kFewWarps = 4;
-constexpr int kFewStages = 3;
+constexpr int kFewStages = 2;
 constexpr int kFewStageBytes = kFewChunk * 2 * kKv4RowBytes;   // K codes, V codes, K scales, V scales
 constexpr int kFewK = 0, kFewV = kFewChunk * 32, kFewKs = 2 * kFewChunk * 32, kFewVs = kFewKs + kFewChunk * 4;
 
@@ -47,11 +55,22 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// d = a b + c
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                        float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    mma_f16(d, a, b0, b1, d[0], d[1], d[2], d[3]);
+}
+// 2^x, off by 2 ulp at most; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t y;
@@ -91,12 +110,15 @@ __device__ __forceinline__ uint32_t visible_bits(long long j0, long long p, int 
     return m;
 }
 
-template <int NT>
+template <int NT, bool PAIR>
 static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const RowsAttnArgs a) {
-    constexpr int UR = 8 * NT;
+    static_assert(!PAIR || NT == 1, "paired columns: one column tile");
+    constexpr int UR = PAIR ? 4 : 8 * NT;
+    constexpr int NB = PAIR ? 1 : 2;         // unit rows a thread holds scores of, per column tile
+    constexpr int MT = kFewChunk / 16;
     extern __shared__ __align__(128) unsigned char few_smem[];
     __shared__ float sm_m[kFewWarps][UR], sm_l[kFewWarps][UR];
-    __shared__ uint32_t sm_vs[kFewWarps][2][kFewChunk / 2];      // V scales of a chunk, f16, by group
+    __shared__ __align__(8) uint32_t sm_vs[kFewWarps][2][kFewChunk / 2];      // V scales of a chunk, f16, by group
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const StreamRows s = stream_rows(a.r, a.v, blockIdx.z);
@@ -110,46 +132,59 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
 
     // ---- the ring ----
     unsigned char* ring = few_smem + warp * kFewStages * kFewStageBytes;
-    // Pages of the two 16-row halves of a chunk (-1: no rows there)
-    auto half_page = [&](int c, int half) {
-        const long long j = static_cast<long long>(unit_chunk(k, c)) * kFewChunk + half * 16;
-        return c < c_end && j < k.end ? kv_page(a.v, s.slot, static_cast<int>(j) >> a.v.shift) : -1;
-    };
-    int pg0 = half_page(c0, 0), pg1 = half_page(c0, 1);
-    uint32_t bad = 0;                      // two bits per stage: halves without a page
     const int pr_mask = a.v.page_rows - 1;
+    const int part = a.v.page_rows * kKv4RowBytes;               // bytes of a block's K part
+    const unsigned page_bytes = static_cast<unsigned>(a.v.heads) * 2u * part;
+    const unsigned char* base = a.cache + static_cast<long long>(hk) * 2 * part;
+    const int end = static_cast<int>(k.end);
+    // Lanes 0..3: page of the chunk's quarter (16 rows) `lane`, -1 where there are no rows.
+    auto quarter_page = [&](int c) {
+        int pg = -1;
+        if (lane < 4 && c < c_end) {
+            const int j = unit_chunk(k, c) * kFewChunk + lane * 16;
+            if (j < end) pg = kv_page(a.v, s.slot, j >> a.v.shift);
+        }
+        return pg;
+    };
+    int pg = quarter_page(c0);
+    uint32_t bad = 0;                      // four bits per stage: quarters without a page
     auto issue = [&](int c, int stage) {
         if (c < c_end) {
-            unsigned char* dst = ring + stage * kFewStageBytes;
+            unsigned char* dst = ring + stage * kFewStageBytes + lane * 16;
             const int j = unit_chunk(k, c) * kFewChunk;
-            const int part = a.v.page_rows * kKv4RowBytes;       // bytes of a block's K part
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int pg = half ? pg1 : pg0;
-                if (pg < 0) continue;
-                const int pr = (j + half * 16) & pr_mask;
-                const unsigned char* blk = a.cache + kv4_block(a.v, pg, hk);
-                cp_async16(dst + kFewK + half * 512 + lane * 16, blk + pr * 32 + lane * 16);
-                cp_async16(dst + kFewV + half * 512 + lane * 16, blk + part + pr * 32 + lane * 16);
-                if (lane < 8)
-                    cp_async16(dst + (lane < 4 ? kFewKs : kFewVs) + half * 64 + (lane & 3) * 16,
-                               blk + (lane < 4 ? 0 : part) + a.v.page_rows * 32 + pr * 4 + (lane & 3) * 16);
+            for (int qu = 0; qu < 4; ++qu) {
+                const int p = __shfl_sync(0xffffffffu, pg, qu);
+                const unsigned char* src =
+                    base + static_cast<unsigned long long>(static_cast<unsigned>(p)) * page_bytes +
+                    (((j + qu * 16) & pr_mask) * 32 + lane * 16);
+                if (p >= 0) {
+                    cp_async16(dst + kFewK + qu * 512, src);
+                    cp_async16(dst + kFewV + qu * 512, src + part);
+                }
             }
-            bad = (bad & ~(3u << (2 * stage))) | (((pg0 < 0 ? 1u : 0u) | (pg1 < 0 ? 2u : 0u)) << (2 * stage));
-            pg0 = half_page(c + kFewWarps, 0);
-            pg1 = half_page(c + kFewWarps, 1);
+            {   // scales: 16 pieces of four rows each of K, then of V
+                const int p = __shfl_sync(0xffffffffu, pg, (lane & 15) >> 2);
+                const unsigned char* src =
+                    base + static_cast<unsigned long long>(static_cast<unsigned>(p)) * page_bytes +
+                    ((lane & 16) ? part : 0) + (a.v.page_rows * 32 + ((j + (lane & 15) * 4) & pr_mask) * 4);
+                if (p >= 0) cp_async16(dst + kFewKs, src);
+            }
+            bad = (bad & ~(15u << (4 * stage))) | ((__ballot_sync(0xffffffffu, pg < 0) & 15u) << (4 * stage));
+            pg = quarter_page(c + kFewWarps);
         }
         cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kFewStages - 1; ++i) issue(c0 + i * kFewWarps, i);
+    issue(c0, 0);
 
-    // ---- Q^T fragments: unit row g of each tile, dims 8 t .. 8 t + 7 of both groups ----
-    uint32_t qh[NT][4][2], ql[NT][4][2];
-    float qs[NT][2];                       // score factors of unit rows 2 t, 2 t + 1
+    // ---- Q^T fragments: column g of each tile, dims 8 t .. 8 t + 7 of both groups ----
+    uint32_t qf[NB][NT][4][2];             // PAIR: one part per column; else high, low
+    // score factors of this thread's rows; -8 sum(q) of columns 2 t, 2 t + 1: where the accumulators
+    // start, and (not PAIR) the remainders' part times the factor
+    float qs[NT][NB], off[NT][2][2], rem[NT][2][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int u = nt * 8 + g;
+        const int u = PAIR ? g >> 1 : nt * 8 + g;
         float x[2][8];
         if (u < k.n_u) {
             const int ur = k.u0 + u, i = ur / a.group, h = hk * a.group + ur % a.group;
@@ -173,180 +208,261 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
         // the row's largest element goes to [2^10, 2^11); rows below 2^-100 are taken as that small
         const int e = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 10 - e) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - 10 + e) << 23) * (0.125f * kLog2e);
+        const float down = (e > 112 ? INFINITY : __uint_as_float(static_cast<uint32_t>(127 - 10 + 24 + e) << 23)) *
+                           (0.125f * kLog2e);
+        float sum[2][2] = {};                // [group][integer part (PAIR: this column's part), remainder]
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             const float* y = x[ks >> 1];
-            const int j = (ks & 1) * 2;
-            split_f16(y[j] * up, y[j + 4] * up, qh[nt][ks][0], ql[nt][ks][0]);
-            split_f16(y[j + 1] * up, y[j + 5] * up, qh[nt][ks][1], ql[nt][ks][1]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int j = (ks & 1) * 2 + b;
+                const float f = b ? 0.0625f : 1.0f;
+                const float y0 = y[j] * up, y1 = y[j + 4] * up, h0 = rintf(y0), h1 = rintf(y1);
+                const __half2 hi = __floats2half2_rn(h0 * f, h1 * f), lo = __floats2half2_rn((y0 - h0) * f, (y1 - h1) * f);
+                const float2 lf = __half22float2(lo);
+                const float sh = h0 + h1, sl = (lf.x + lf.y) * (b ? 16.0f : 1.0f);
+                if (PAIR) {
+                    qf[0][nt][ks][b] = h2_bits((g & 1) ? lo : hi);
+                    sum[ks >> 1][0] += (g & 1) ? sl : sh;
+                } else {
+                    qf[0][nt][ks][b] = h2_bits(hi);
+                    qf[NB - 1][nt][ks][b] = h2_bits(lo);
+                    sum[ks >> 1][0] += sh;
+                    sum[ks >> 1][1] += sl;
+                }
+            }
         }
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+            for (int part = 0; part < (PAIR ? 1 : 2); ++part) {
+                float v = sum[gr][part];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                v *= -8.0f / 16777216.0f;
+                if (part) v *= down;
+                (part ? rem : off)[nt][gr][0] = __shfl_sync(0xffffffffu, v, 8 * t);
+                (part ? rem : off)[nt][gr][1] = __shfl_sync(0xffffffffu, v, 8 * t + 4);
+            }
         qs[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
-        qs[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+        if (!PAIR) qs[nt][NB - 1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
     }
 
-    // ---- running state: unit rows 8 nt + 2 t, + 1; O^T dims 8 g + 2 mt, + 1 ----
-    float m[NT][2], l[NT][2], o[NT][4][4];
+    // ---- running state: unit row 8 nt + 2 t + b (PAIR: t); O^T dims 8 g + 2 mt, + 1 ----
+    auto row_of = [&](int nt, int b) { return PAIR ? t : nt * 8 + 2 * t + b; };
+    float m[NT][NB], l[NT][NB], o[NT][4][4];
     int E = -1000;                         // V is held times 2^(11 - E)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            m[nt][b] = -INFINITY;
+            l[nt][b] = 0.0f;
+        }
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[nt][mt][j] = 0.0f;
     }
     const long long p_first = s.pos0 + k.u0 / a.group, p_last = s.pos0 + (k.u0 + k.n_u - 1) / a.group;
+    // chunks whose 64 keys all rows see: below, and above or within the sinks
+    const int full_hi = static_cast<int>(min(p_first - (kFewChunk - 1), 0x7fffff00ll));
+    const int full_lo = a.window == 0 ? 0 : static_cast<int>(max(0ll, min(p_last - a.window + 1, 0x7fffff00ll)));
     const int key_a = (g >> 1) + 4 * (g & 1);           // key of S^T row g of a 16-key half
 
     int stage = 0;
     for (int c = c0; c < c_end; c += kFewWarps) {
-        issue(c + (kFewStages - 1) * kFewWarps, stage == 0 ? kFewStages - 1 : stage - 1);
+        issue(c + kFewWarps, stage ^ 1);
         cp_async_wait<kFewStages - 1>();
         __syncwarp();
         const unsigned char* st = ring + stage * kFewStageBytes;
-        const long long j0 = static_cast<long long>(unit_chunk(k, c)) * kFewChunk;
-        const uint32_t halves = (bad >> (2 * stage)) & 3u;
-        const uint32_t have = ((halves & 1u) ? 0u : 0xffffu) | ((halves & 2u) ? 0u : 0xffff0000u);
+        const int j0 = unit_chunk(k, c) * kFewChunk;
+        const uint32_t miss = (bad >> (4 * stage)) & 15u;
+        const bool full = miss == 0 && j0 <= full_hi && (j0 >= full_lo || j0 + kFewChunk <= a.sinks);
 
-        // rows 2 t, 2 t + 1 of each tile: the keys of this chunk they see
-        uint32_t vis[NT][2];
-        const bool full = have == 0xffffffffu && j0 + 31 <= p_first &&
-                          (a.window == 0 || j0 > p_last - a.window || j0 + 31 < a.sinks);
+        // this thread's rows: the keys of this chunk they see
+        uint32_t vis[NT][NB][2];
+        uint32_t have[2] = {0xffffffffu, 0xffffffffu};
         if (full) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) vis[nt][0] = vis[nt][1] = 0xffffffffu;
-        } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const long long p = s.pos0 + (k.u0 + nt * 8 + 2 * t + b) / a.group;
-                    vis[nt][b] = visible_bits(j0, p, a.window, a.sinks) & have;
-                }
+                for (int b = 0; b < NB; ++b) vis[nt][b][0] = vis[nt][b][1] = 0xffffffffu;
+        } else {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                have[w] = ((miss >> (2 * w)) & 1u ? 0u : 0xffffu) | ((miss >> (2 * w)) & 2u ? 0u : 0xffff0000u);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        vis[nt][b][w] = visible_bits(j0 + 32 * w, s.pos0 + (k.u0 + row_of(nt, b)) / a.group, a.window,
+                                                     a.sinks) & have[w];
+            }
         }
 
-        // V scales: lane = key; f16 of scale 2^(11 - E), 0 for keys without a page, no unit row or a
-        // scale that is not a number (those keys' outputs are set below)
+        // V scales, lane = keys `lane` and 32 + lane: f16 of scale 2^(11 - E), 0 for keys without a page
+        // or row, and for a scale that is not a number (those keys' outputs are set below)
         float fac = 1.0f;
-        uint32_t nan0, nan1;
+        uint32_t any_nan;
+        uint32_t vw[2];
         {
-            uint32_t w = *reinterpret_cast<const uint32_t*>(st + kFewVs + lane * 4);
-            const bool dead = !((have >> lane) & 1u) || j0 + lane > p_last;
-            if (dead) w = 0;
-            nan0 = __ballot_sync(0xffffffffu, (w & 0x7f80u) == 0x7f80u);
-            nan1 = __ballot_sync(0xffffffffu, (w & 0x7f800000u) == 0x7f800000u);
-            if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-            if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
-            const uint32_t big = __reduce_max_sync(0xffffffffu, max(w & 0xffffu, w >> 16));
+            uint32_t big = 0;
+            bool nan = false;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                vw[w] = *reinterpret_cast<const uint32_t*>(st + kFewVs + (32 * w + lane) * 4);
+                if (!full && (!((have[w] >> lane) & 1u) || j0 + 32 * w + lane > p_last)) vw[w] = 0;
+                big = max(big, max(vw[w] & 0xffffu, vw[w] >> 16));
+            }
+            nan = big >= 0x7f80u;
+            any_nan = __ballot_sync(0xffffffffu, nan);
+            uint32_t z[2] = {vw[0], vw[1]};
+            if (any_nan) {
+                big = 0;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if ((z[w] & 0xffffu) >= 0x7f80u) z[w] &= 0xffff0000u;
+                    if ((z[w] >> 16) >= 0x7f80u) z[w] &= 0xffffu;
+                    big = max(big, max(z[w] & 0xffffu, z[w] >> 16));
+                }
+            }
+            big = __reduce_max_sync(0xffffffffu, big);
             const int e = static_cast<int>(big >> 7) - 127;
             if (big != 0 && e > E) {
                 fac = E < e - 120 ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 + E - e) << 23);
                 E = e;
             }
-            auto scaled = [&](uint32_t b) {            // bf16 bits -> f32 of value 2^(11 - E)
-                const int ne = static_cast<int>(b >> 7) - E + 11;
-                return b == 0 || ne <= 0 ? 0.0f : __uint_as_float((static_cast<uint32_t>(ne) << 23) | ((b & 0x7fu) << 16));
+            const int shift = E == -1000 ? 0 : (11 - E) * (1 << 23);      // (every scale is 0 so far)
+            auto scaled = [&](uint32_t b) {                // f32 bits of a bf16 scale -> times 2^(11 - E)
+                const int r = static_cast<int>(b) + shift;
+                return b == 0 || r < 0x00800000 ? 0.0f : __int_as_float(r);
             };
             // slot of key 16 a + 4 i + t in the order its reader wants: 16 a + 4 t + i
             const int at = (lane & 16) | ((lane & 3) << 2) | ((lane >> 2) & 3);
-            reinterpret_cast<__half*>(sm_vs[warp][0])[at] = __float2half_rn(scaled(w & 0xffffu));
-            reinterpret_cast<__half*>(sm_vs[warp][1])[at] = __float2half_rn(scaled(w >> 16));
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                reinterpret_cast<__half*>(sm_vs[warp][0])[32 * w + at] = __float2half_rn(scaled(z[w] << 16));
+                reinterpret_cast<__half*>(sm_vs[warp][1])[32 * w + at] = __float2half_rn(scaled(z[w] & 0xffff0000u));
+            }
         }
         __syncwarp();
 
-        // ---- scores ----
-        float sc[NT][2][4];
+        // ---- scores: sc[..][mt][j] of keys 16 mt + key_a + 8 j ----
+        float sc[NT][NB][MT][2];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < MT; ++mt) {
             uint32_t ka[4][4];              // A fragments of the four 16-dim steps
 #pragma unroll
             for (int hi = 0; hi < 2; ++hi) {
                 const uint2 w = *reinterpret_cast<const uint2*>(st + kFewK + (mt * 16 + hi * 8 + key_a) * 32 + t * 8);
-                uint32_t p0[4], p1[4];
-                kv4_pairs(w.x, p0);
-                kv4_pairs(w.y, p1);
-                ka[0][hi] = p0[0], ka[0][2 + hi] = p0[1], ka[1][hi] = p0[2], ka[1][2 + hi] = p0[3];
-                ka[2][hi] = p1[0], ka[2][2 + hi] = p1[1], ka[3][hi] = p1[2], ka[3][2 + hi] = p1[3];
+                const uint32_t x8 = w.x >> 8, y8 = w.y >> 8;
+                ka[0][hi] = w.x & 0x000f000fu, ka[0][2 + hi] = w.x & 0x00f000f0u;
+                ka[1][hi] = x8 & 0x000f000fu, ka[1][2 + hi] = x8 & 0x00f000f0u;
+                ka[2][hi] = w.y & 0x000f000fu, ka[2][2 + hi] = w.y & 0x00f000f0u;
+                ka[3][hi] = y8 & 0x000f000fu, ka[3][2 + hi] = y8 & 0x00f000f0u;
             }
-            const uint32_t wa = *reinterpret_cast<const uint32_t*>(st + kFewKs + (mt * 16 + key_a) * 4);
-            const uint32_t wb = *reinterpret_cast<const uint32_t*>(st + kFewKs + (mt * 16 + 8 + key_a) * 4);
-            const float ka0 = __uint_as_float(wa << 16), ka1 = __uint_as_float(wa & 0xffff0000u);
-            const float kb0 = __uint_as_float(wb << 16), kb1 = __uint_as_float(wb & 0xffff0000u);
+            float ks0[2], ks1[2];           // the keys' scales
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(st + kFewKs + (mt * 16 + 8 * j + key_a) * 4);
+                ks0[j] = __uint_as_float(w << 16);
+                ks1[j] = __uint_as_float(w & 0xffff0000u);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float d0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                float d0[4], d1[4];
+                const float* c0v = off[nt][0];
+                const float* c1v = off[nt][1];
+                mma_f16(d0, ka[0], qf[0][nt][0][0], qf[0][nt][0][1], c0v[0], c0v[1], c0v[0], c0v[1]);
+                mma_f16(d1, ka[2], qf[0][nt][2][0], qf[0][nt][2][1], c1v[0], c1v[1], c1v[0], c1v[1]);
+                mma_f16(d0, ka[1], qf[0][nt][1][0], qf[0][nt][1][1]);
+                mma_f16(d1, ka[3], qf[0][nt][3][0], qf[0][nt][3][1]);
+                if (!PAIR) {
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    mma_f16(d0, ka[ks], ql[nt][ks][0], ql[nt][ks][1]);
-                    mma_f16(d1, ka[2 + ks], ql[nt][2 + ks][0], ql[nt][2 + ks][1]);
-                }
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    mma_f16(d0, ka[ks], qh[nt][ks][0], qh[nt][ks][1]);
-                    mma_f16(d1, ka[2 + ks], qh[nt][2 + ks][0], qh[nt][2 + ks][1]);
+                    for (int ks = 0; ks < 2; ++ks) {
+                        mma_f16(d0, ka[ks], qf[NB - 1][nt][ks][0], qf[NB - 1][nt][ks][1]);
+                        mma_f16(d1, ka[2 + ks], qf[NB - 1][nt][2 + ks][0], qf[NB - 1][nt][2 + ks][1]);
+                    }
                 }
                 // the row's factor first: scale times raw sum could leave f32's range
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float f = qs[nt][j & 1];
-                    sc[nt][mt][j] = fmaf(d1[j] * f, j < 2 ? ka1 : kb1, (d0[j] * f) * (j < 2 ? ka0 : kb0));
-                }
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const float f = qs[nt][b];
+                        const float r0 = PAIR ? (d0[2 * j] + d0[2 * j + 1]) * f : fmaf(d0[2 * j + b], f, rem[nt][0][b]);
+                        const float r1 = PAIR ? (d1[2 * j] + d1[2 * j + 1]) * f : fmaf(d1[2 * j + b], f, rem[nt][1][b]);
+                        sc[nt][b][mt][j] = fmaf(r1, ks1[j], r0 * ks0[j]);
+                    }
             }
         }
         if (!full) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (!((vis[nt][j & 1] >> (mt * 16 + (j >> 1) * 8 + key_a)) & 1u)) sc[nt][mt][j] = -INFINITY;
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (!((vis[nt][b][mt >> 1] >> ((mt & 1) * 16 + j * 8 + key_a)) & 1u))
+                                sc[nt][b][mt][j] = -INFINITY;
         }
 
         // ---- softmax ----
-        uint32_t ph[NT][2][2], pl[NT][2][2];
-        float corr[NT][2];
+        uint32_t ph[NT][MT][2], pl[PAIR ? 1 : NT][MT][2];       // B fragments of P^T (PAIR: both parts in ph)
+        float corr[NT][NB];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float mx = fmaxf(fmaxf(sc[nt][0][b], sc[nt][0][b + 2]), fmaxf(sc[nt][1][b], sc[nt][1][b + 2]));
+            for (int b = 0; b < NB; ++b) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(sc[nt][b][mt][0], sc[nt][b][mt][1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                 const float mn = fmaxf(m[nt][b], mx);
                 // nothing seen yet: exp2(-inf - 0) = 0 keeps every term 0
-                const float base = mn == -INFINITY ? 0.0f : mn;
-                corr[nt][b] = exp2f(m[nt][b] - base);
+                const float bs = mn == -INFINITY ? 0.0f : mn;
+                corr[nt][b] = ex2(m[nt][b] - bs);
                 m[nt][b] = mn;
                 float sum = 0.0f;
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    sc[nt][mt][b] = exp2f(sc[nt][mt][b] - base + 12.0f);
-                    sc[nt][mt][b + 2] = exp2f(sc[nt][mt][b + 2] - base + 12.0f);
-                    sum += sc[nt][mt][b] + sc[nt][mt][b + 2];
-                }
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        sc[nt][b][mt][j] = ex2(sc[nt][b][mt][j] - bs + 12.0f);
+                        sum += sc[nt][b][mt][j];
+                    }
                 l[nt][b] = fmaf(l[nt][b], corr[nt][b], sum);
                 corr[nt][b] *= fac;
             }
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-                uint32_t h0, l0, h1, l1;
-                split_f16(sc[nt][mt][0], sc[nt][mt][1], h0, l0);
-                split_f16(sc[nt][mt][2], sc[nt][mt][3], h1, l1);
-                ph[nt][mt][0] = movmatrix_trans(h0);
-                ph[nt][mt][1] = movmatrix_trans(h1);
-                pl[nt][mt][0] = movmatrix_trans(l0);
-                pl[nt][mt][1] = movmatrix_trans(l1);
+            for (int mt = 0; mt < MT; ++mt) {
+                if (PAIR) {
+                    uint32_t h, lo;          // keys j = 0, 1; then (high, low) of each
+                    split_f16(sc[nt][0][mt][0], sc[nt][0][mt][1], h, lo);
+                    ph[nt][mt][0] = movmatrix_trans(__byte_perm(h, lo, 0x5410));
+                    ph[nt][mt][1] = movmatrix_trans(__byte_perm(h, lo, 0x7632));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t h, lo;
+                        split_f16(sc[nt][0][mt][j], sc[nt][NB - 1][mt][j], h, lo);
+                        ph[nt][mt][j] = movmatrix_trans(h);
+                        pl[nt][mt][j] = movmatrix_trans(lo);
+                    }
+                }
             }
         }
 
         // ---- values ----
-        uint32_t va[2][4][4];              // A fragments: 16-key step, dim tile
+        float d[NT][4][4];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+        for (int ks = 0; ks < MT; ++ks) {
             const unsigned char* vp = st + kFewV + ks * 512 + t * 32 + g * 4;
             const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vp), w1 = *reinterpret_cast<const uint32_t*>(vp + 128);
             const uint32_t w2 = *reinterpret_cast<const uint32_t*>(vp + 256);
@@ -360,37 +476,46 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
             kv4_pairs(__byte_perm(w2, w3, 0x7632), d23 + 4);
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                va[ks][mt][0] = h2_bits(__hmul2(bits_h2(d01[2 * mt]), bits_h2(vs.x)));
-                va[ks][mt][1] = h2_bits(__hmul2(bits_h2(d01[2 * mt + 1]), bits_h2(vs.x)));
-                va[ks][mt][2] = h2_bits(__hmul2(bits_h2(d23[2 * mt]), bits_h2(vs.y)));
-                va[ks][mt][3] = h2_bits(__hmul2(bits_h2(d23[2 * mt + 1]), bits_h2(vs.y)));
+                uint32_t va[4];
+                va[0] = h2_bits(__hmul2(bits_h2(d01[2 * mt]), bits_h2(vs.x)));
+                va[1] = h2_bits(__hmul2(bits_h2(d01[2 * mt + 1]), bits_h2(vs.x)));
+                va[2] = h2_bits(__hmul2(bits_h2(d23[2 * mt]), bits_h2(vs.y)));
+                va[3] = h2_bits(__hmul2(bits_h2(d23[2 * mt + 1]), bits_h2(vs.y)));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (ks == 0)
+                        mma_f16(d[nt][mt], va, ph[nt][0][0], ph[nt][0][1], 0.0f, 0.0f, 0.0f, 0.0f);
+                    else
+                        mma_f16(d[nt][mt], va, ph[nt][ks][0], ph[nt][ks][1]);
+                    if (!PAIR) mma_f16(d[nt][mt], va, pl[nt][ks][0], pl[nt][ks][1]);
+                }
             }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_f16(d, va[0][mt], pl[nt][0][0], pl[nt][0][1]);
-                mma_f16(d, va[1][mt], pl[nt][1][0], pl[nt][1][1]);
-                mma_f16(d, va[0][mt], ph[nt][0][0], ph[nt][0][1]);
-                mma_f16(d, va[1][mt], ph[nt][1][0], ph[nt][1][1]);
+            for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[nt][mt][j] = fmaf(o[nt][mt][j], corr[nt][j & 1], d[j]);
+                for (int j = 0; j < 4; ++j)
+                    o[nt][mt][j] = fmaf(o[nt][mt][j], corr[nt][PAIR ? 0 : j & 1], d[nt][mt][j]);
+        if (any_nan) {                     // a seen key whose V group is not a number
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const uint32_t n0 = __ballot_sync(0xffffffffu, (vw[w] & 0xffffu) >= 0x7f80u);
+                const uint32_t n1 = __ballot_sync(0xffffffffu, (vw[w] >> 16) >= 0x7f80u);
+                const uint32_t bits = g < 4 ? n0 : n1;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        if (vis[nt][b][w] & bits) {
+#pragma unroll
+                            for (int mt = 0; mt < 4; ++mt) o[nt][mt][b] = o[nt][mt][b + 2] = __uint_as_float(0x7fc00000u);
+                        }
             }
-        if (nan0 | nan1) {                 // a seen key whose V group is not a number
-            const uint32_t bits = g < 4 ? nan0 : nan1;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    if (vis[nt][b] & bits) {
-#pragma unroll
-                        for (int mt = 0; mt < 4; ++mt) o[nt][mt][b] = o[nt][mt][b + 2] = __uint_as_float(0x7fc00000u);
-                    }
         }
         __syncwarp();
-        stage = stage + 1 == kFewStages ? 0 : stage + 1;
+        stage ^= 1;
     }
     cp_async_wait<0>();
     __syncthreads();
@@ -404,20 +529,23 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NB; ++b) {
             float sum = l[nt][b];
             sum += __shfl_xor_sync(0xffffffffu, sum, 4);
             sum += __shfl_xor_sync(0xffffffffu, sum, 8);
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-            const int u = nt * 8 + 2 * t + b;
+            const int u = row_of(nt, b);
             if (g == 0) {
                 sm_m[warp][u] = m[nt][b];
                 sm_l[warp][u] = sum;
             }
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int mt = 0; mt < 4; ++mt) {
+                const float x = PAIR ? o[nt][mt][0] + o[nt][mt][1] : o[nt][mt][b];
+                const float y = PAIR ? o[nt][mt][2] + o[nt][mt][3] : o[nt][mt][b + 2];
                 *reinterpret_cast<float2*>(so + u * (kHeadDim + 4) + 8 * g + 2 * mt) =
-                    make_float2(o[nt][mt][b] * fa * fb, o[nt][mt][b + 2] * fa * fb);
+                    make_float2(x * fa * fb, y * fa * fb);
+            }
         }
     __syncthreads();
     for (int x = tid; x < k.n_u * (kHeadDim / 4); x += kFewWarps * 32) {
@@ -454,9 +582,9 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
     }
 }
 
-inline size_t few_smem_bytes(int nt) {
+inline size_t few_smem_bytes(int unit_rows) {
     const size_t ring = size_t(kFewWarps) * kFewStages * kFewStageBytes;
-    const size_t join = size_t(kFewWarps) * 8 * nt * (kHeadDim + 4) * sizeof(float);
+    const size_t join = size_t(kFewWarps) * unit_rows * (kHeadDim + 4) * sizeof(float);
     return ring > join ? ring : join;
 }
 

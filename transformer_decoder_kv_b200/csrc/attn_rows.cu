@@ -74,7 +74,7 @@ RowsPlan rows_plan(const dec_kv_view& view, const dec_kv_rows& rows, int n_heads
     RowsPlan p;
     const int group = n_heads / view.n_kv_heads;
     const long long u = static_cast<long long>(rows.max_rows) * group;
-    p.unit_rows = u <= 8 ? 8 : 16;
+    p.unit_rows = u <= 4 ? 4 : u <= 8 ? 8 : 16;
     p.tiles = static_cast<int>((u + p.unit_rows - 1) / p.unit_rows);
     const long long units = static_cast<long long>(rows.batch) * view.n_kv_heads * p.tiles;
     const long long chunks = rows_max_chunks(view_dev(view), rows.max_rows, window, sinks, kFewChunk);
@@ -98,14 +98,14 @@ cudaError_t launch_after(K kern, dim3 grid, dim3 block, cudaStream_t st, Args...
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int NT>
+template <int NT, bool PAIR>
 cudaError_t launch_kv4_few(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
+    constexpr int UR = PAIR ? 4 : 8 * NT;
     static_assert(kFewWarps * kFewStages * kFewStageBytes <= 48 * 1024, "no opt-in needed");
-    k_attn_kv4_few<NT><<<dim3(p.S, a.v.heads * p.tiles, a.r.batch), kFewWarps * 32, few_smem_bytes(NT), st>>>(a);
+    k_attn_kv4_few<NT, PAIR><<<dim3(p.S, a.v.heads * p.tiles, a.r.batch), kFewWarps * 32, few_smem_bytes(UR), st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.S == 1) return e;
-    return launch_after(k_attn_merge<8 * NT, kFewChunk>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), dim3(128), st,
-                        a);
+    return launch_after(k_attn_merge<UR, kFewChunk>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), dim3(128), st, a);
 }
 
 template <bool KV4>
@@ -125,7 +125,7 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     if (!bad && !(aligned16(q) && aligned16(out) && aligned16(workspace) && aligned16(cache) && aligned16(k) &&
                   aligned16(v)))
         bad = "q, out, workspace and the caches must be 16-byte aligned";
-    if (!bad && (static_cast<long long>(rows->max_rows) * n_heads + 8 * view->n_kv_heads) / 8 > 65535)
+    if (!bad && (static_cast<long long>(rows->max_rows) * n_heads + 4 * view->n_kv_heads) / 4 > 65535)
         bad = "max_rows * n_heads is too large";
     if (!bad && workspace_bytes < dec_attention_rows_workspace_size(view, rows, n_heads)) bad = "workspace too small";
     if (bad) return rows_fail(who, DEC_EINVAL, bad);
@@ -149,7 +149,9 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     a.min_chunks = plan.min_chunks;
     if (KV4) {
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
-        const cudaError_t e = plan.unit_rows == 8 ? launch_kv4_few<1>(a, plan, st) : launch_kv4_few<2>(a, plan, st);
+        const cudaError_t e = plan.unit_rows == 4   ? launch_kv4_few<1, true>(a, plan, st)
+                              : plan.unit_rows == 8 ? launch_kv4_few<1, false>(a, plan, st)
+                                                    : launch_kv4_few<2, false>(a, plan, st);
         return e == cudaSuccess ? DEC_OK : rows_cuda_fail(who, e, "k_attn_kv4_few launch");
     }
     k_attn_rows<KV4><<<dim3((rows->max_rows + 3) / 4, n_heads, rows->batch), 128, 0,

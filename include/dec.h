@@ -533,8 +533,8 @@ typedef struct dec_kv_rows {
  * Bytes of a 4-bit cache pool (K and V) for `view`: 72 per (row, K/V head) instead of f32's 512;
  * 0 for a bad view. Each (page, head) block holds page_rows rows of K codes (32 bytes each: words
  * of 8 consecutive dims, lowest nibble first, code + 8; K's words in the order 0 4 1 5 2 6 3 7),
- * page_rows K scales (two bf16 each: dims 0..31 and 32..63), then the V codes (words in order) and
- * V scales.
+ * page_rows K scales (two bf16 each: dims 0..31 and 32..63), then the V codes (words
+ * in order, each 16-bit half rotated left by 2) and V scales.
  * Codes: per (row, head, group of 32 dims) a = max |x|, s = a / 7 rounded to f32 and then to bf16
  * (0 when below 2^-126), c = x / s rounded to the nearest integer, ties to even (decided exactly,
  * not on a rounded quotient); the cache stands for c s, within s / 2 of x. A group with a NaN or

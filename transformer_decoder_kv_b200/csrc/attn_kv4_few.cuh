@@ -13,11 +13,11 @@
 //                 within 2^-23 of the row's largest element; dims met as 16 n are divided by 16).
 //                 The code is n - 8, so sum(q n) - 8 sum(q) is wanted: of the integer parts that is exact
 //                 in f32 (below 2^20 for the 32 dims of a group) and the accumulators just start at
-//                 -8 sum; the remainders' correction is added with the row's factor. One accumulator per
+//                 -8 sum; the remainders' correction is added to the result. One accumulator per
 //                 group; the key's two scales and the row's factor are applied in f32.
 //   softmax       running maximum per unit row and warp, p = exp2(s - m + 12), f32 sums.
 //   O^T += V^T P^T  A = 64 dims x 16 keys: code times scale, 3 + 8 significant bits, exact in f16
-//                 after the warp's power of two 2^-E (E follows the largest scale met so far);
+//                 after the warp's power of two 2^(9 - E) (E follows the largest scale met so far);
 //                 B = p in f16 high and low parts. Each chunk of 64 keys sums into fresh
 //                 accumulators that are added to the running f32 sums by ordinary fma, so that the
 //                 tensor cores' truncation does not build up over a long cache.
@@ -88,16 +88,13 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32
     lo = h2_bits(__floats2half2_rn(x - f.x, y - f.y));
 }
 
-// Codes of nibbles j and j + 4 of a word as f16 pairs p[j], j = 0..3. 0x6400 | n is 1024 + n; a nibble
-// four bits up gives 1024 + 16 n, halved down by one fma.
-__device__ __forceinline__ void kv4_pairs(uint32_t w, uint32_t* p) {
-    const __half2 sub = bits_h2(0x64086408u);                              // 1032
-    const __half2 s16 = bits_h2(0x2c002c00u), sub16 = bits_h2(0xd480d480u);   // 1 / 16, -72
-    const uint32_t w8 = w >> 8;
-    p[0] = h2_bits(__hsub2(bits_h2((w & 0x000f000fu) | 0x64006400u), sub));
-    p[1] = h2_bits(__hfma2(bits_h2((w & 0x00f000f0u) | 0x64006400u), s16, sub16));
-    p[2] = h2_bits(__hsub2(bits_h2((w8 & 0x000f000fu) | 0x64006400u), sub));
-    p[3] = h2_bits(__hfma2(bits_h2((w8 & 0x00f000f0u) | 0x64006400u), s16, sub16));
+// Four dims of two keys (the 16-bit halves of u, V's layout: codes at bits 2, 6, 10 and around 14) times
+// the keys' scales s: x = 1 + n / 16 by its bits, then x (16 s) - 1.5 (16 s) = (n - 8) s, exact: 1.5 times 8
+// significant bits is 10, the result has 11.
+__device__ __forceinline__ void kv4_values(uint32_t u, __half2 s16, __half2 c, uint32_t* v) {
+    const uint32_t x[4] = {u << 4, u, u >> 4, __byte_perm(u, 0, 0x2301)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = h2_bits(__hfma2(bits_h2((x[i] & 0x03c003c0u) | 0x3c003c00u), s16, c));
 }
 
 // Positions j0 .. j0 + 31 a query at position p sees, as bits.
@@ -137,40 +134,39 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
     const unsigned page_bytes = static_cast<unsigned>(a.v.heads) * 2u * part;
     const unsigned char* base = a.cache + static_cast<long long>(hk) * 2 * part;
     const int end = static_cast<int>(k.end);
-    // Lanes 0..3: page of the chunk's quarter (16 rows) `lane`, -1 where there are no rows.
+    const int* tab = a.v.table ? a.v.table + s.slot * a.v.pages_per_slot : nullptr;
+    // Lane: pieces of the chunk's 16-row quarter lane / 8, by 8 lanes each.
+    const int sub = lane & 7, qrow = (lane >> 3) * 16;
+    const int scale_off = a.v.page_rows * 32 + (sub & 3) * 16 + ((sub & 4) ? part : 0);
+    // Page of the lane's quarter of a chunk, -1 where there are no rows.
     auto quarter_page = [&](int c) {
-        int pg = -1;
-        if (lane < 4 && c < c_end) {
-            const int j = unit_chunk(k, c) * kFewChunk + lane * 16;
-            if (j < end) pg = kv_page(a.v, s.slot, j >> a.v.shift);
+        int p = -1;
+        const int j = unit_chunk(k, c) * kFewChunk + qrow;
+        if (c < c_end && j < end) {
+            p = tab ? tab[j >> a.v.shift] : s.slot * a.v.pages_per_slot + (j >> a.v.shift);
+            if (static_cast<unsigned>(p) >= static_cast<unsigned>(a.v.n_pages)) p = -1;
         }
-        return pg;
+        return p;
     };
     int pg = quarter_page(c0);
-    uint32_t bad = 0;                      // four bits per stage: quarters without a page
+    uint32_t bad[2] = {0, 0};              // per stage: lanes whose quarter has no page
     auto issue = [&](int c, int stage) {
         if (c < c_end) {
-            unsigned char* dst = ring + stage * kFewStageBytes + lane * 16;
-            const int j = unit_chunk(k, c) * kFewChunk;
+            unsigned char* dst = ring + stage * kFewStageBytes;
+            const int r = (unit_chunk(k, c) * kFewChunk + qrow) & pr_mask;
+            const unsigned char* blk = base + static_cast<unsigned long long>(static_cast<unsigned>(pg)) * page_bytes;
+            const unsigned char* src = blk + (r * 32 + sub * 16);
+            if (pg >= 0) {
+                unsigned char* d = dst + qrow * 32 + sub * 16;
 #pragma unroll
-            for (int qu = 0; qu < 4; ++qu) {
-                const int p = __shfl_sync(0xffffffffu, pg, qu);
-                const unsigned char* src =
-                    base + static_cast<unsigned long long>(static_cast<unsigned>(p)) * page_bytes +
-                    (((j + qu * 16) & pr_mask) * 32 + lane * 16);
-                if (p >= 0) {
-                    cp_async16(dst + kFewK + qu * 512, src);
-                    cp_async16(dst + kFewV + qu * 512, src + part);
-                }
+                for (int i = 0; i < 4; ++i) cp_async16(d + kFewK + i * 128, src + i * 128);
+                src += part;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cp_async16(d + kFewV + i * 128, src + i * 128);
+                cp_async16(dst + ((sub & 4) ? kFewVs : kFewKs) + qrow * 4 + (sub & 3) * 16, blk + (r * 4 + scale_off));
             }
-            {   // scales: 16 pieces of four rows each of K, then of V
-                const int p = __shfl_sync(0xffffffffu, pg, (lane & 15) >> 2);
-                const unsigned char* src =
-                    base + static_cast<unsigned long long>(static_cast<unsigned>(p)) * page_bytes +
-                    ((lane & 16) ? part : 0) + (a.v.page_rows * 32 + ((j + (lane & 15) * 4) & pr_mask) * 4);
-                if (p >= 0) cp_async16(dst + kFewKs, src);
-            }
-            bad = (bad & ~(15u << (4 * stage))) | ((__ballot_sync(0xffffffffu, pg < 0) & 15u) << (4 * stage));
+            const uint32_t m = __ballot_sync(0xffffffffu, pg < 0);
+            if (stage) bad[1] = m; else bad[0] = m;
             pg = quarter_page(c + kFewWarps);
         }
         cp_async_commit();
@@ -180,7 +176,7 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
     // ---- Q^T fragments: column g of each tile, dims 8 t .. 8 t + 7 of both groups ----
     uint32_t qf[NB][NT][4][2];             // PAIR: one part per column; else high, low
     // score factors of this thread's rows; -8 sum(q) of columns 2 t, 2 t + 1: where the accumulators
-    // start, and (not PAIR) the remainders' part times the factor
+    // start, and (not PAIR) the remainders' part
     float qs[NT][NB], off[NT][2][2], rem[NT][2][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -241,7 +237,6 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
                 v += __shfl_xor_sync(0xffffffffu, v, 1);
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
                 v *= -8.0f / 16777216.0f;
-                if (part) v *= down;
                 (part ? rem : off)[nt][gr][0] = __shfl_sync(0xffffffffu, v, 8 * t);
                 (part ? rem : off)[nt][gr][1] = __shfl_sync(0xffffffffu, v, 8 * t + 4);
             }
@@ -251,13 +246,13 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
 
     // ---- running state: unit row 8 nt + 2 t + b (PAIR: t); O^T dims 8 g + 2 mt, + 1 ----
     auto row_of = [&](int nt, int b) { return PAIR ? t : nt * 8 + 2 * t + b; };
-    float m[NT][NB], l[NT][NB], o[NT][4][4];
-    int E = -1000;                         // V is held times 2^(11 - E)
+    float m[NT][NB], rf[NT][NB], l[NT][NB], o[NT][4][4];     // maximum, reference of the weights, sum, values
+    int E = -100;                          // V is held times 2^(9 - E)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            m[nt][b] = -INFINITY;
+            m[nt][b] = rf[nt][b] = -INFINITY;
             l[nt][b] = 0.0f;
         }
 #pragma unroll
@@ -278,7 +273,7 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
         __syncwarp();
         const unsigned char* st = ring + stage * kFewStageBytes;
         const int j0 = unit_chunk(k, c) * kFewChunk;
-        const uint32_t miss = (bad >> (4 * stage)) & 15u;
+        const uint32_t miss = stage ? bad[1] : bad[0];
         const bool full = miss == 0 && j0 <= full_hi && (j0 >= full_lo || j0 + kFewChunk <= a.sinks);
 
         // this thread's rows: the keys of this chunk they see
@@ -292,7 +287,7 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
         } else {
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                have[w] = ((miss >> (2 * w)) & 1u ? 0u : 0xffffu) | ((miss >> (2 * w)) & 2u ? 0u : 0xffff0000u);
+                have[w] = ((miss >> (16 * w)) & 1u ? 0u : 0xffffu) | ((miss >> (16 * w)) & 0x100u ? 0u : 0xffff0000u);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -302,50 +297,45 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
             }
         }
 
-        // V scales, lane = keys `lane` and 32 + lane: f16 of scale 2^(11 - E), 0 for keys without a page
-        // or row, and for a scale that is not a number (those keys' outputs are set below)
+        // V scales, lane = two keys 4 apart: f16 of 16 times scale 2^(9 - E), 0 for keys without a page
+        // or row, and for a scale that is not a number (those keys' outputs are set below). Kept in
+        // the order their readers want: keys 16 i + t, + 4, + 8, + 12 of quad lane t side by side.
         float fac = 1.0f;
         uint32_t any_nan;
+        const int vkey = (lane >> 3) * 16 + ((lane >> 1) & 3) + 8 * (lane & 1);
         uint32_t vw[2];
         {
-            uint32_t big = 0;
-            bool nan = false;
+            float z[2][2], big = 0.0f;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                vw[w] = *reinterpret_cast<const uint32_t*>(st + kFewVs + (32 * w + lane) * 4);
-                if (!full && (!((have[w] >> lane) & 1u) || j0 + 32 * w + lane > p_last)) vw[w] = 0;
-                big = max(big, max(vw[w] & 0xffffu, vw[w] >> 16));
+                const int key = vkey + 4 * w;
+                vw[w] = *reinterpret_cast<const uint32_t*>(st + kFewVs + key * 4);
+                if (!full && ((((lane & 16) ? have[1] : have[0]) >> (key & 31) & 1u) == 0u || j0 + key > p_last)) vw[w] = 0;
+                z[w][0] = __uint_as_float(vw[w] << 16);
+                z[w][1] = __uint_as_float(vw[w] & 0xffff0000u);
+                big = fmaxf(big, fmaxf(z[w][0], z[w][1]));
             }
-            nan = big >= 0x7f80u;
-            any_nan = __ballot_sync(0xffffffffu, nan);
-            uint32_t z[2] = {vw[0], vw[1]};
+            // (stored scales are below 2^126: four of them stay finite)
+            any_nan = __ballot_sync(0xffffffffu, !((z[0][0] + z[0][1]) + (z[1][0] + z[1][1]) < INFINITY));
             if (any_nan) {
-                big = 0;
+                big = 0.0f;
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if ((z[w] & 0xffffu) >= 0x7f80u) z[w] &= 0xffff0000u;
-                    if ((z[w] >> 16) >= 0x7f80u) z[w] &= 0xffffu;
-                    big = max(big, max(z[w] & 0xffffu, z[w] >> 16));
-                }
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int gr = 0; gr < 2; ++gr) {
+                        if (!(z[w][gr] < INFINITY)) z[w][gr] = 0.0f;
+                        big = fmaxf(big, z[w][gr]);
+                    }
             }
-            big = __reduce_max_sync(0xffffffffu, big);
-            const int e = static_cast<int>(big >> 7) - 127;
-            if (big != 0 && e > E) {
+            const int e = max(static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23) - 127, -100);
+            if (e > E) {
                 fac = E < e - 120 ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 + E - e) << 23);
                 E = e;
             }
-            const int shift = E == -1000 ? 0 : (11 - E) * (1 << 23);      // (every scale is 0 so far)
-            auto scaled = [&](uint32_t b) {                // f32 bits of a bf16 scale -> times 2^(11 - E)
-                const int r = static_cast<int>(b) + shift;
-                return b == 0 || r < 0x00800000 ? 0.0f : __int_as_float(r);
-            };
-            // slot of key 16 a + 4 i + t in the order its reader wants: 16 a + 4 t + i
-            const int at = (lane & 16) | ((lane & 3) << 2) | ((lane >> 2) & 3);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - E) << 23);
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                reinterpret_cast<__half*>(sm_vs[warp][0])[32 * w + at] = __float2half_rn(scaled(z[w] << 16));
-                reinterpret_cast<__half*>(sm_vs[warp][1])[32 * w + at] = __float2half_rn(scaled(z[w] & 0xffff0000u));
-            }
+            for (int gr = 0; gr < 2; ++gr)
+                sm_vs[warp][gr][lane] = h2_bits(__floats2half2_rn(z[0][gr] * up, z[1][gr] * up));
         }
         __syncwarp();
 
@@ -386,15 +376,15 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
                         mma_f16(d1, ka[2 + ks], qf[NB - 1][nt][2 + ks][0], qf[NB - 1][nt][2 + ks][1]);
                     }
                 }
-                // the row's factor first: scale times raw sum could leave f32's range
+                // (the raw sums are below 1: no scale takes them out of f32's range)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         const float f = qs[nt][b];
-                        const float r0 = PAIR ? (d0[2 * j] + d0[2 * j + 1]) * f : fmaf(d0[2 * j + b], f, rem[nt][0][b]);
-                        const float r1 = PAIR ? (d1[2 * j] + d1[2 * j + 1]) * f : fmaf(d1[2 * j + b], f, rem[nt][1][b]);
-                        sc[nt][b][mt][j] = fmaf(r1, ks1[j], r0 * ks0[j]);
+                        const float r0 = PAIR ? d0[2 * j] + d0[2 * j + 1] : d0[2 * j + b] + rem[nt][0][b];
+                        const float r1 = PAIR ? d1[2 * j] + d1[2 * j + 1] : d1[2 * j + b] + rem[nt][1][b];
+                        sc[nt][b][mt][j] = fmaf(r1, ks1[j], r0 * ks0[j]) * f;
                     }
             }
         }
@@ -425,16 +415,19 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                 const float mn = fmaxf(m[nt][b], mx);
-                // nothing seen yet: exp2(-inf - 0) = 0 keeps every term 0
-                const float bs = mn == -INFINITY ? 0.0f : mn;
-                corr[nt][b] = ex2(m[nt][b] - bs);
+                // Weights are 2^(s - ref): ref 12 below the maximum keeps small ones in f16's range
+                // (at the maximum itself where f32 no longer resolves 12); before anything is seen
+                // ref 0 makes every term 0.
+                const float ref = mn == -INFINITY ? 0.0f : fabsf(mn) < 65536.0f ? mn - 12.0f : mn;
+                corr[nt][b] = ex2(rf[nt][b] - ref);
                 m[nt][b] = mn;
+                rf[nt][b] = mn == -INFINITY ? -INFINITY : ref;
                 float sum = 0.0f;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        sc[nt][b][mt][j] = ex2(sc[nt][b][mt][j] - bs + 12.0f);
+                        sc[nt][b][mt][j] = ex2(sc[nt][b][mt][j] - ref);
                         sum += sc[nt][b][mt][j];
                     }
                 l[nt][b] = fmaf(l[nt][b], corr[nt][b], sum);
@@ -469,18 +462,16 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
             const uint32_t w3 = *reinterpret_cast<const uint32_t*>(vp + 384);
             const uint2 vs = *reinterpret_cast<const uint2*>(&sm_vs[warp][g >> 2][ks * 8 + t * 2]);
             // pairs along the keys: low and high halves of two keys' words side by side
+            const __half2 s0 = bits_h2(vs.x), s1 = bits_h2(vs.y), c15 = __float2half2_rn(-1.5f);
+            const __half2 z0 = __hmul2(s0, c15), z1 = __hmul2(s1, c15);
             uint32_t d01[8], d23[8];
-            kv4_pairs(__byte_perm(w0, w1, 0x5410), d01);
-            kv4_pairs(__byte_perm(w0, w1, 0x7632), d01 + 4);
-            kv4_pairs(__byte_perm(w2, w3, 0x5410), d23);
-            kv4_pairs(__byte_perm(w2, w3, 0x7632), d23 + 4);
+            kv4_values(__byte_perm(w0, w1, 0x5410), s0, z0, d01);
+            kv4_values(__byte_perm(w0, w1, 0x7632), s0, z0, d01 + 4);
+            kv4_values(__byte_perm(w2, w3, 0x5410), s1, z1, d23);
+            kv4_values(__byte_perm(w2, w3, 0x7632), s1, z1, d23 + 4);
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                uint32_t va[4];
-                va[0] = h2_bits(__hmul2(bits_h2(d01[2 * mt]), bits_h2(vs.x)));
-                va[1] = h2_bits(__hmul2(bits_h2(d01[2 * mt + 1]), bits_h2(vs.x)));
-                va[2] = h2_bits(__hmul2(bits_h2(d23[2 * mt]), bits_h2(vs.y)));
-                va[3] = h2_bits(__hmul2(bits_h2(d23[2 * mt + 1]), bits_h2(vs.y)));
+                const uint32_t va[4] = {d01[2 * mt], d01[2 * mt + 1], d23[2 * mt], d23[2 * mt + 1]};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     if (ks == 0)
@@ -501,9 +492,16 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
         if (any_nan) {                     // a seen key whose V group is not a number
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                const uint32_t n0 = __ballot_sync(0xffffffffu, (vw[w] & 0xffffu) >= 0x7f80u);
-                const uint32_t n1 = __ballot_sync(0xffffffffu, (vw[w] >> 16) >= 0x7f80u);
-                const uint32_t bits = g < 4 ? n0 : n1;
+                // of keys 32 w .. 32 w + 31: those with such a scale, from the lanes that hold them
+                uint32_t bits = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t n0 = __ballot_sync(0xffffffffu, (vw[i] & 0x7f80u) == 0x7f80u);
+                    const uint32_t n1 = __ballot_sync(0xffffffffu, (vw[i] & 0x7f800000u) == 0x7f800000u);
+                    const uint32_t n = g < 4 ? n0 : n1;
+                    for (int x = 16 * w; x < 16 * w + 16; ++x)
+                        if ((n >> x) & 1u) bits |= 1u << (((x >> 3) & 1) * 16 + ((x >> 1) & 3) + 8 * (x & 1) + 4 * i);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -520,12 +518,9 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
     cp_async_wait<0>();
     __syncthreads();
 
-    // ---- join the warps: O as [unit row][dim], each warp's sums scaled back by 2^(E - 11) ----
+    // ---- join the warps: O as [unit row][dim], each warp's sums scaled back by 2^(E - 9) ----
     float* so = reinterpret_cast<float*>(few_smem) + warp * UR * (kHeadDim + 4);
-    // 2^(E - 11) in two factors, so that neither leaves f32's range
-    const int es = max(E - 11, -250), ea = es / 2, eb = es - ea;
-    const float fa = __uint_as_float(static_cast<uint32_t>(127 + ea) << 23);
-    const float fb = __uint_as_float(static_cast<uint32_t>(127 + eb) << 23);
+    const float back = __uint_as_float(static_cast<uint32_t>(127 + E - 9) << 23);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -536,7 +531,7 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
             const int u = row_of(nt, b);
             if (g == 0) {
-                sm_m[warp][u] = m[nt][b];
+                sm_m[warp][u] = rf[nt][b];
                 sm_l[warp][u] = sum;
             }
 #pragma unroll
@@ -544,7 +539,7 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
                 const float x = PAIR ? o[nt][mt][0] + o[nt][mt][1] : o[nt][mt][b];
                 const float y = PAIR ? o[nt][mt][2] + o[nt][mt][3] : o[nt][mt][b + 2];
                 *reinterpret_cast<float2*>(so + u * (kHeadDim + 4) + 8 * g + 2 * mt) =
-                    make_float2(x * fa * fb, y * fa * fb);
+                    make_float2(x * back, y * back);
             }
         }
     __syncthreads();

@@ -79,8 +79,15 @@ RowsPlan rows_plan(const dec_kv_view& view, const dec_kv_rows& rows, int n_heads
     const long long units = static_cast<long long>(rows.batch) * view.n_kv_heads * p.tiles;
     const long long chunks = rows_max_chunks(view_dev(view), rows.max_rows, window, sinks, kFewChunk);
     p.min_chunks = kFewWarps;
-    const long long want = (8ll * kRowsSms + units - 1) / units, most = chunks / p.min_chunks;
-    p.S = static_cast<int>(std::max(1ll, std::min({want, most, static_cast<long long>(kRowsMaxSplits)})));
+    // Fewest (waves of resident blocks) x (rounds of chunks per warp, and one for the block's start and
+    // end); a merge costs about one more.
+    const long long slots = kRowsSms * (p.unit_rows == 4 ? 4 : p.unit_rows == 8 ? 3 : 2);
+    long long best = 0;
+    for (int S = 1; S <= kRowsMaxSplits && (S == 1 || chunks / S >= p.min_chunks); ++S) {
+        const long long rounds = ((chunks + S - 1) / S + kFewWarps - 1) / kFewWarps;
+        const long long cost = (units * S + slots - 1) / slots * (rounds + 1) + (S > 1);
+        if (S == 1 || cost < best) best = cost, p.S = S;
+    }
     return p;
 }
 

@@ -82,11 +82,13 @@ __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const 
                     for (int j = 0; j < 8; ++j) w |= static_cast<uint32_t>(kv4_code(e[j], sc, inv) + 8) << (4 * j);
                 }
             }
-            *codes = w;
+            // V's halves are kept rotated left by 2, as the attention kernels unpack them
+            *codes = which ? ((w << 2) & 0xfffcfffcu) | ((w >> 14) & 0x00030003u) : w;
             if ((l8 & 3) == 0) *scale = static_cast<uint16_t>(sb);
         } else {
             float e[8];
-            const uint32_t w = ok ? *codes : 0x88888888u;
+            uint32_t w = ok ? *codes : 0x88888888u;
+            if (which && ok) w = ((w >> 2) & 0x3fff3fffu) | ((w << 14) & 0xc000c000u);
             const float sc = ok ? __uint_as_float(static_cast<uint32_t>(*scale) << 16) : 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) e[j] = sc * static_cast<float>(static_cast<int>((w >> (4 * j)) & 15u) - 8);

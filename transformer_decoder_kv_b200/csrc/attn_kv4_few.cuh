@@ -563,17 +563,7 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
                 acc.w = fmaf(e, ow.w, acc.w);
             }
         }
-        const int ur = k.u0 + u, h = hk * a.group + ur % a.group;
-        const long long row = s.row0 + ur / a.group;
-        if (k.splits == 1) {
-            const bool ok = L > 0.0f && isfinite(L);
-            *reinterpret_cast<float4*>(a.out + row * a.out_ld + h * kHeadDim + d4 * 4) =
-                ok ? make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        } else {
-            float* p = a.part + ((row * a.heads + h) * a.S + sp) * kPartStride;
-            if (d4 == 0) *reinterpret_cast<float2*>(p) = make_float2(mx, L);
-            *reinterpret_cast<float4*>(p + 4 + d4 * 4) = acc;
-        }
+        store_unit_row(a, k, s, hk, sp, u, d4, mx, L, acc);
     }
 }
 

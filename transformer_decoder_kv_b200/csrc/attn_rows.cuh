@@ -87,6 +87,22 @@ __host__ __device__ __forceinline__ int split_begin(const UnitKeys& k, int sp) {
     return static_cast<int>(static_cast<long long>(k.total) * sp / k.splits);
 }
 
+// A block's result of unit row u, dims 4 d4 .. 4 d4 + 3: the output, or this split's partial state.
+__device__ __forceinline__ void store_unit_row(const RowsAttnArgs& a, const UnitKeys& k, const StreamRows& s, int hk,
+                                               int sp, int u, int d4, float m, float l, float4 o) {
+    const int ur = k.u0 + u, h = hk * a.group + ur % a.group;
+    const long long row = s.row0 + ur / a.group;
+    if (k.splits == 1) {
+        const bool ok = l > 0.0f && isfinite(l);
+        *reinterpret_cast<float4*>(a.out + row * a.out_ld + h * kHeadDim + d4 * 4) =
+            ok ? make_float4(o.x / l, o.y / l, o.z / l, o.w / l) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    } else {
+        float* p = a.part + ((row * a.heads + h) * a.S + sp) * kPartStride;
+        if (d4 == 0) *reinterpret_cast<float2*>(p) = make_float2(m, l);
+        *reinterpret_cast<float4*>(p + 4 + d4 * 4) = o;
+    }
+}
+
 // Chunks of the widest unit, from the sizes the host knows.
 inline long long rows_max_chunks(const KvViewDev& v, int max_rows, int window, int sinks, int ck) {
     const long long cap = kv_capacity(v);

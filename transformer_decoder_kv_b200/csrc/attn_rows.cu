@@ -5,6 +5,7 @@
 #include "attn_f32_few.cuh"
 #include "attn_kv4_few.cuh"
 #include "attn_rows.cuh"
+#include "attn_rows_tc.cuh"
 
 using namespace dec;
 
@@ -12,7 +13,8 @@ namespace {
 
 // Launch shape of a batch: unit rows per block, units per (stream, K/V head), splits per unit.
 struct RowsPlan {
-    int unit_rows, tiles, S, min_chunks;
+    int unit_rows, S, min_chunks;
+    long long tiles;
     int most_splits;          // what the workspace is sized for
 };
 
@@ -24,7 +26,14 @@ RowsPlan rows_plan(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, i
     RowsPlan p{};
     const long long u = static_cast<long long>(rows.max_rows) * (n_heads / view.n_kv_heads);
     int resident, warps, chunk;
-    if (kv4) {
+    // The tensor-core tiles of 128 rows pay from the second unit of the widest few-row variant on.
+    if (u > (kv4 ? 32 : 8)) {
+        p.unit_rows = kRtRows;
+        resident = 2;
+        warps = 1;
+        chunk = kRtKeys;
+        p.min_chunks = 1;
+    } else if (kv4) {
         p.unit_rows = u <= 4 ? 4 : u <= 8 ? 8 : 16;
         resident = u <= 4 ? 4 : u <= 8 ? 3 : 2;
         warps = kFewWarps;
@@ -37,7 +46,7 @@ RowsPlan rows_plan(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, i
         chunk = kF32Chunk;
         p.min_chunks = 2 * kF32Warps;
     }
-    p.tiles = static_cast<int>((u + p.unit_rows - 1) / p.unit_rows);
+    p.tiles = (u + p.unit_rows - 1) / p.unit_rows;
     const long long units = static_cast<long long>(rows.batch) * view.n_kv_heads * p.tiles;
     const long long slots = static_cast<long long>(kRowsSms) * resident;
     const KvViewDev v = view_dev(view);
@@ -73,15 +82,27 @@ template <int NT, bool PAIR>
 cudaError_t launch_kv4_few(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
     constexpr int UR = PAIR ? 4 : 8 * NT;
     static_assert(kFewWarps * kFewStages * kFewStageBytes <= 48 * 1024, "no opt-in needed");
-    k_attn_kv4_few<NT, PAIR><<<dim3(p.S, a.v.heads * p.tiles, a.r.batch), kFewWarps * 32, few_smem_bytes(UR), st>>>(a);
+    k_attn_kv4_few<NT, PAIR><<<dim3(p.S, static_cast<unsigned>(a.v.heads * p.tiles), a.r.batch), kFewWarps * 32, few_smem_bytes(UR), st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.S == 1) return e;
     return launch_after(k_attn_merge<UR, kFewChunk>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), dim3(128), st, a);
 }
 
+template <bool KV4>
+cudaError_t launch_rows_tc(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
+    thread_local int attr_dev = -1;
+    cudaError_t e = prefer_max_shared_once(k_attn_rows_tc<KV4>, attr_dev, rt_smem_bytes<KV4>());
+    if (e != cudaSuccess) return e;
+    k_attn_rows_tc<KV4><<<dim3(p.S, static_cast<unsigned>(a.v.heads * p.tiles), a.r.batch), kRtThreads, rt_smem_bytes<KV4>(), st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.S == 1) return e;
+    return launch_after(k_attn_merge<kRtRows, kRtKeys>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), dim3(128), st,
+                        a);
+}
+
 template <int R>
 cudaError_t launch_f32_few(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
-    k_attn_f32_few<R><<<dim3(p.S, a.v.heads * p.tiles, a.r.batch), kF32Warps * 32, 0, st>>>(a);
+    k_attn_f32_few<R><<<dim3(p.S, static_cast<unsigned>(a.v.heads * p.tiles), a.r.batch), kF32Warps * 32, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.S == 1) return e;
     return launch_after(k_attn_merge<R, kF32Chunk>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), dim3(128), st, a);
@@ -104,9 +125,12 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     if (!bad && !(aligned16(q) && aligned16(out) && aligned16(workspace) && aligned16(cache) && aligned16(k) &&
                   aligned16(v)))
         bad = "q, out, workspace and the caches must be 16-byte aligned";
-    if (!bad && static_cast<long long>(rows->max_rows) * n_heads / 8 + view->n_kv_heads > 65535)
-        bad = "max_rows * n_heads is too large";
     if (!bad && workspace_bytes < dec_attention_rows_workspace_size(view, rows, n_heads)) bad = "workspace too small";
+    RowsPlan plan{};
+    if (!bad) {
+        plan = rows_plan(KV4, *view, *rows, n_heads, window, sinks);
+        if (plan.tiles * view->n_kv_heads > 65535) bad = "max_rows * n_heads is too large";
+    }
     if (bad) return rows_fail(who, DEC_EINVAL, bad);
     RowsAttnArgs a{};
     a.v = view_dev(*view);
@@ -122,13 +146,14 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     a.sinks = sinks;
     a.out = out;
     a.out_ld = out_ld;
-    const RowsPlan plan = rows_plan(KV4, *view, *rows, n_heads, window, sinks);
     a.part = static_cast<float*>(workspace);
     a.S = plan.S;
     a.min_chunks = plan.min_chunks;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (KV4)
+    if (plan.unit_rows == kRtRows)
+        e = launch_rows_tc<KV4>(a, plan, st);
+    else if (KV4)
         e = plan.unit_rows == 4   ? launch_kv4_few<1, true>(a, plan, st)
             : plan.unit_rows == 8 ? launch_kv4_few<1, false>(a, plan, st)
                                   : launch_kv4_few<2, false>(a, plan, st);

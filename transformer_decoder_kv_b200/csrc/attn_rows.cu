@@ -51,7 +51,7 @@ RowsPlan rows_plan(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, i
     const long long slots = static_cast<long long>(kRowsSms) * resident;
     const KvViewDev v = view_dev(view);
     const long long chunks = rows_max_chunks(v, rows.max_rows, window, sinks, chunk);
-    const long long cap = std::max(1ll, std::min<long long>(kRowsMaxSplits, 2 * slots / units));
+    const long long cap = std::max(1ll, std::min<long long>(kRowsMaxSplits, (p.unit_rows == kRtRows ? 3 : 2) * slots / units));
     p.most_splits = static_cast<int>(
         std::max(1ll, std::min(cap, rows_max_chunks(v, rows.max_rows, 0, 0, chunk) / p.min_chunks)));
     p.S = 1;
@@ -60,6 +60,7 @@ RowsPlan rows_plan(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, i
         const long long rounds = ((chunks + S - 1) / S + warps - 1) / warps;
         const long long cost = (units * S + slots - 1) / slots * (rounds + 1) + (S > 1);
         if (S == 1 || cost < best) best = cost, p.S = S;
+        if (p.unit_rows == kRtRows) p.S = S;
     }
     return p;
 }

@@ -13,10 +13,12 @@
 //               tile's product is read back and added to the running f32 sums in registers, scaled by
 //               the change of the maximum, so that the tensor cores' truncation does not build up.
 //
-// A block (256 threads, two per SM) goes through load, unpack, MMA, softmax, MMA, add one after the
-// other; the other block of the SM fills the gaps. An M128 N128 K16 MMA takes 65 SM cycles and an
-// M128 N64 K16 one 45 to 49 (measured), 1240 per tile of a 4-bit cache; the softmax's instructions, about
-// 8 per score, are the larger part of a tile's time.
+// A block (256 threads, two per SM) alternates between its softmax and the two products, and unpacks
+// the next tile's K while P V runs and its V while Q K^T runs; the other block of the SM fills the gaps.
+// A 4-bit cache's tile is copied into shared memory by cp.async one tile ahead; an f32 tile goes
+// through registers. An M128 N128 K16 MMA takes 65 SM cycles and an M128 N64 K16 one 45 to 49
+// (measured), 1240 per tile of a 4-bit cache; the softmax, about 6 instructions per score and an exp2
+// unit that takes 1024 cycles per tile, is the larger part of a tile's time.
 //
 // A tile that holds a NaN or an infinity in K or V, at a position that some row sees, is computed by a
 // plain f32 loop instead: in a matrix product it would reach the rows that do not see it.
@@ -30,9 +32,12 @@ namespace dec {
 constexpr int kRtRows = 128, kRtKeys = 128, kRtThreads = 256;
 constexpr int kRtPlane = kRtRows * 128;           // one f16 operand plane: 128 rows of 64 dims
 constexpr uint32_t kRtTmemCols = 256;             // S / P 0..127, O 128..191
+// a tile of a 4-bit cache as it lies: K codes, V codes, K scales, V scales
+constexpr int kRtStage = kRtKeys * 2 * kKv4RowBytes;
+constexpr int kRtV = kRtKeys * 32, kRtKs = 2 * kRtKeys * 32, kRtVs = kRtKs + kRtKeys * 4;
 template <bool KV4>
 constexpr int rt_smem_bytes() {
-    return (2 + (KV4 ? 2 : 4)) * kRtPlane + 1024;
+    return (2 + (KV4 ? 2 : 4)) * kRtPlane + (KV4 ? 2 * kRtStage : 0) + 1024;
 }
 
 __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -70,19 +75,45 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&r)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(x[i]);
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&x)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&r)[16]) {
+    uint32_t x[16];
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(x[0]),
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]),
+          "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+        : "r"(addr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(x[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&x)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(x[0]),
         "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]),
-        "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]), "r"(x[16]), "r"(x[17]), "r"(x[18]), "r"(x[19]),
-        "r"(x[20]), "r"(x[21]), "r"(x[22]), "r"(x[23]), "r"(x[24]), "r"(x[25]), "r"(x[26]), "r"(x[27]), "r"(x[28]),
-        "r"(x[29]), "r"(x[30]), "r"(x[31]), "r"(addr)
+        "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]), "r"(addr)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+// Packed f32 pairs: a * b + c and a + b on both halves.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // One row's (or key's) 16-byte chunk c of a 128-byte-swizzled operand plane.
@@ -129,10 +160,12 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     unsigned char* sQ = smem;                                    // high, low
     unsigned char* sK = smem + 2 * kRtPlane;                     // high (, low)
     unsigned char* sV = sK + (KV4 ? 1 : 2) * kRtPlane;
+    unsigned char* stages = sV + kRtPlane;                       // KV4: two
     __shared__ __align__(8) uint64_t bar_s, bar_o;
     __shared__ uint32_t s_tmem;
     __shared__ float sm_f[kRtRows], sm_x[2][kRtRows];            // row factors; column halves' maxima, sums
-    __shared__ uint32_t sm_kmax[2][8], sm_vmax[2][8], sm_bad[2][8], sm_nan[2][8];   // of a tile, per loading warp
+    __shared__ uint32_t sm_bad[2][8];                            // of a tile's 16-key blocks: no page
+    __shared__ uint32_t sm_kmax[8], sm_vmax[8];                     // f32: magnitudes
     __shared__ int s_fail;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -145,7 +178,8 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     const int c0 = split_begin(k, sp), c_end = split_begin(k, sp + 1);
     const int end = static_cast<int>(k.end);
     const long long p_first = s.pos0 + k.u0 / a.group, p_last = s.pos0 + (k.u0 + k.n_u - 1) / a.group;
-    const long long seen_lo = a.window > 0 ? p_first - a.window + 1 : 0;     // keys below, past the sinks: no row sees them
+    // keys below, past the sinks: no row sees them
+    const int seen_lo = a.window > 0 ? static_cast<int>(max(0ll, min(p_first - a.window + 1, 0x7fffff00ll))) : 0;
 
     if (tid == 0) {
         mbar_init(&bar_s, 1);
@@ -162,83 +196,38 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     const int kr = tid >> 1, kh = tid & 1;
     const int* tab = a.v.table ? a.v.table + s.slot * a.v.pages_per_slot : nullptr;
     const int pr_mask = a.v.shift == 31 ? 0x7fffffff : a.v.page_rows - 1;
-    auto key_page = [&](int c) {                   // page of this thread's key, -1 where no row sees one
-        if (c >= c_end) return -1;
-        const int j = unit_chunk(k, c) * kRtKeys + kr;
-        if (j >= end || (j < seen_lo && j >= a.sinks)) return -1;
+    auto page_of = [&](int j) {                    // of a key below `end`; -1: no page
         const int p = tab ? tab[j >> a.v.shift] : s.slot * a.v.pages_per_slot + (j >> a.v.shift);
         return static_cast<unsigned>(p) < static_cast<unsigned>(a.v.n_pages) ? p : -1;
     };
-    uint4 kc, vc;                                  // KV4: codes of 32 dims
-    uint32_t ksw, vsw;                             // KV4: scales
-    float4 kf[KV4 ? 1 : 8], vf[KV4 ? 1 : 8];       // f32: 32 dims
-    auto load = [&](int c, int page) {
-        const int pr = (unit_chunk(k, c) * kRtKeys + kr) & pr_mask;
-        if (KV4) {
-            kc = vc = make_uint4(0, 0, 0, 0);
-            ksw = vsw = 0;
-            if (page >= 0) {
+    auto key_page = [&](int c) {
+        if (c >= c_end) return -1;
+        const int j = unit_chunk(k, c) * kRtKeys + kr;
+        return j < end ? page_of(j) : -1;
+    };
+    auto seen = [&](int j) { return j < end && (j >= seen_lo || j < a.sinks); };
+    // Copies the tile into its stage (4-bit cache), and notes its blocks without a page.
+    auto stage_tile = [&](int c, int page) {
+        const int buf = (c - c0) & 1;
+        if (c < c_end) {
+            if (KV4 && page >= 0) {
+                const int pr = (unit_chunk(k, c) * kRtKeys + kr) & pr_mask;
                 const int part = a.v.page_rows * kKv4RowBytes;
                 const unsigned char* blk = a.cache + kv4_block(a.v, page, hk);
-                kc = *reinterpret_cast<const uint4*>(blk + pr * 32 + kh * 16);
-                vc = *reinterpret_cast<const uint4*>(blk + part + pr * 32 + kh * 16);
-                ksw = *reinterpret_cast<const uint32_t*>(blk + a.v.page_rows * 32 + pr * 4);
-                vsw = *reinterpret_cast<const uint32_t*>(blk + part + a.v.page_rows * 32 + pr * 4);
+                unsigned char* dst = stages + buf * kRtStage;
+                cp_async16(dst + tid * 16, blk + pr * 32 + kh * 16);
+                cp_async16(dst + kRtV + tid * 16, blk + part + pr * 32 + kh * 16);
+                if ((kr & 3) == 0)                 // four keys' scales of K, of V
+                    cp_async16(dst + (kh ? kRtVs : kRtKs) + kr * 4, blk + kh * part + a.v.page_rows * 32 + pr * 4);
             }
-        } else {
-            const long long off = page < 0 ? 0 : kvf_block(a.v, page, hk) + static_cast<long long>(pr) * kHeadDim + kh * 32;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                kf[i] = vf[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (page >= 0) {
-                    kf[i] = __ldg(reinterpret_cast<const float4*>(a.k + off) + i);
-                    vf[i] = __ldg(reinterpret_cast<const float4*>(a.vv + off) + i);
-                }
-            }
+            if (lane == 0) sm_bad[buf][warp] = page < 0 && unit_chunk(k, c) * kRtKeys + kr < end;
         }
-    };
-    // Largest magnitudes of the loaded tile (f32 bits), what is not finite, and 16-key blocks without a
-    // page, per loading warp (its 16 keys) into buffer `buf`.
-    auto survey = [&](int c, int page, int buf) {
-        uint32_t km = 0, vm = 0, nan = 0;
-        auto take = [&](uint32_t bits, uint32_t& m) {
-            if (bits >= 0x7f800000u) nan = 1; else m = max(m, bits);
-        };
-        if (KV4) {
-            take(ksw << 16, km), take(ksw & 0xffff0000u, km);
-            take(vsw << 16, vm), take(vsw & 0xffff0000u, vm);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                take(__float_as_uint(fabsf(kf[i].x)), km), take(__float_as_uint(fabsf(kf[i].y)), km);
-                take(__float_as_uint(fabsf(kf[i].z)), km), take(__float_as_uint(fabsf(kf[i].w)), km);
-                take(__float_as_uint(fabsf(vf[i].x)), vm), take(__float_as_uint(fabsf(vf[i].y)), vm);
-                take(__float_as_uint(fabsf(vf[i].z)), vm), take(__float_as_uint(fabsf(vf[i].w)), vm);
-            }
-        }
-        km = __reduce_max_sync(0xffffffffu, km);
-        vm = __reduce_max_sync(0xffffffffu, vm);
-        nan = __reduce_max_sync(0xffffffffu, nan);
-        // a key may be left out as unseen in a block that has a page: only the page decides here
-        uint32_t bad = 0;
-        if (c < c_end) {
-            const int j = unit_chunk(k, c) * kRtKeys + warp * 16;
-            if (j < end) {
-                const int p = tab ? tab[j >> a.v.shift] : s.slot * a.v.pages_per_slot + (j >> a.v.shift);
-                bad = static_cast<unsigned>(p) >= static_cast<unsigned>(a.v.n_pages);
-            }
-        }
-        (void)page;
-        if (lane == 0) {
-            sm_kmax[buf][warp] = km;
-            sm_vmax[buf][warp] = vm;
-            sm_nan[buf][warp] = nan;
-            sm_bad[buf][warp] = bad;
-        }
+        if (KV4) cp_async_commit();
     };
 
     int page = key_page(c0);
-    load(c0, page);
+    stage_tile(c0, page);
+    int page_next = key_page(c0 + 1);
 
     // ---- queries: thread = row tid / 2, half of its dims ----
     {
@@ -269,47 +258,217 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         for (int w = 0; w < 4; ++w) rt_store_split<KV4>(sQ, sQ + kRtPlane, kr, kh * 4 + w, x + 8 * w);
         if (kh == 0) sm_f[kr] = pow2i(e - 10) * (0.125f * kLog2e);
     }
-    survey(c0, page, 0);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = s_tmem;
 
     // ---- rows: thread = row 32 (warp % 4) + lane, columns 64 half .. of S and 32 half .. of O ----
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * 64;
-    const uint32_t t_o = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128 + half * 32;
-    const float f_row = sm_f[row];
     const long long p_row = s.pos0 + (k.u0 + min(row, k.n_u - 1)) / a.group;
     float o[32], m = -INFINITY, ref_old = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-    int E = -100;                                  // V is held times 2^(vbits - E)
     constexpr int vbits = KV4 ? 9 : 10;
-    uint32_t ph = 0;                               // MMA rounds done: the barriers' phase
+    int ek = -100, E = -100;                       // K is held times 2^(10 - ek), V times 2^(vbits - E)
+    float fac = 1.0f;                              // what the last change of E makes of O
+    auto raise_E = [&](int e) {
+        const int n = max(E, e);
+        fac = E < n - 120 ? 0.0f : pow2i(E - n);
+        E = n;
+    };
+    uint32_t bad = 0;                              // blocks of the tile at hand without a page
+
+    // Looks a tile over before its K is unpacked: powers of two, blocks without a page. True when
+    // something that a row sees is not finite.
+    auto survey4 = [&](int c) {
+        const int buf = (c - c0) & 1, j0 = unit_chunk(k, c) * kRtKeys;
+        bad = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) bad |= sm_bad[buf][w] << w;
+        const bool live = bad == 0 && j0 + kRtKeys <= end && (j0 >= seen_lo || j0 + kRtKeys <= a.sinks);
+        const unsigned char* st = stages + buf * kRtStage + lane * 16;
+        const uint4 kv = *reinterpret_cast<const uint4*>(st + kRtKs), vv = *reinterpret_cast<const uint4*>(st + kRtVs);
+        const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, vw[4] = {vv.x, vv.y, vv.z, vv.w};
+        uint32_t km = 0, vm = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (live || (seen(j0 + lane * 4 + i) && !((bad >> (lane >> 2)) & 1u))) {
+                km = max(km, max(kw[i] & 0xffffu, kw[i] >> 16));
+                vm = max(vm, max(vw[i] & 0xffffu, vw[i] >> 16));
+            }
+        km = __reduce_max_sync(0xffffffffu, km);
+        vm = __reduce_max_sync(0xffffffffu, vm);
+        if (max(km, vm) >= 0x7f80u) return true;
+        ek = max(static_cast<int>(km >> 7) - 127, -100);
+        raise_E(max(static_cast<int>(vm >> 7) - 127, -100));
+        return false;
+    };
+    auto live_key = [&](int c) {
+        return seen(unit_chunk(k, c) * kRtKeys + kr) && !((bad >> (kr >> 4)) & 1u);
+    };
+    // Unpacks K (times 2^(10 - ek)).
+    auto unpack_k4 = [&](int c) {
+        const unsigned char* st = stages + ((c - c0) & 1) * kRtStage;
+        const uint4 kc = *reinterpret_cast<const uint4*>(st + tid * 16);
+        const uint32_t ksw = live_key(c) ? *reinterpret_cast<const uint32_t*>(st + kRtKs + kr * 4) : 0u;
+        const float ku = pow2i(10 - ek);
+        const __half2 k0 = __float2half2_rn(__uint_as_float(ksw << 16) * ku);
+        const __half2 k1 = __float2half2_rn(__uint_as_float(ksw & 0xffff0000u) * ku);
+        const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w};
+        const __half2 sub = bits_h2(0x64086408u), s16 = bits_h2(0x2c002c00u), sub16 = bits_h2(0xd480d480u);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            // words 2 kh + w / 2 (+ 4 for odd w). 0x6400 | n is 1024 + n; a nibble four bits up gives
+            // 1024 + 16 n
+            const __half2 sc = (w & 1) ? k1 : k0;
+            const uint32_t x = kw[w], x8 = x >> 8;
+            uint4 r;
+            r.x = h2_bits(__hmul2(__hsub2(bits_h2((x & 0x000f000fu) | 0x64006400u), sub), sc));
+            r.y = h2_bits(__hmul2(__hfma2(bits_h2((x & 0x00f000f0u) | 0x64006400u), s16, sub16), sc));
+            r.z = h2_bits(__hmul2(__hsub2(bits_h2((x8 & 0x000f000fu) | 0x64006400u), sub), sc));
+            r.w = h2_bits(__hmul2(__hfma2(bits_h2((x8 & 0x00f000f0u) | 0x64006400u), s16, sub16), sc));
+            *rt_chunk(sK, kr, 2 * kh + (w >> 1) + 4 * (w & 1)) = r;
+        }
+    };
+    // Unpacks V (16 times the scale is 2^(13 - E) times it). A word's nibbles i and 4 + i come out
+    // paired: the order 0 4 1 5 2 6 3 7 again.
+    auto unpack_v4 = [&](int c) {
+        const unsigned char* st = stages + ((c - c0) & 1) * kRtStage;
+        const uint4 vc = *reinterpret_cast<const uint4*>(st + kRtV + tid * 16);
+        const uint32_t vsw = live_key(c) ? *reinterpret_cast<const uint32_t*>(st + kRtVs + kr * 4) : 0u;
+        const __half2 v0 = __float2half2_rn(__uint_as_float(kh ? vsw & 0xffff0000u : vsw << 16) * pow2i(13 - E));
+        const __half2 z0 = __hmul2(v0, __float2half2_rn(-1.5f));
+        const uint32_t vw[4] = {vc.x, vc.y, vc.z, vc.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t v[4];
+            kv4_values(vw[w], v0, z0, v);
+            *rt_chunk(sV, kr, 4 * kh + w) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    };
+    // f32: this thread's 32 dims of K or V, 0 where no row sees the key.
+    auto load_f32 = [&](int c, int pg, const float* pool, float4 (&x)[8]) {
+        const int j = unit_chunk(k, c) * kRtKeys + kr;
+        const bool live = pg >= 0 && seen(j);
+        const float4* src = reinterpret_cast<const float4*>(
+            pool + (live ? kvf_block(a.v, pg, hk) + static_cast<long long>(j & pr_mask) * kHeadDim + kh * 32 : 0));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = live ? __ldg(src + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    // f32: largest magnitude, as bits (a NaN's are above all).
+    auto magnitude = [&](const float4 (&x)[8]) {
+        uint32_t g = 0;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+            g = max(max(max(g, __float_as_uint(fabsf(x[n].x))), __float_as_uint(fabsf(x[n].y))),
+                    max(__float_as_uint(fabsf(x[n].z)), __float_as_uint(fabsf(x[n].w))));
+        return g;
+    };
+    // f32: scales, splits and stores.
+    auto store_f32 = [&](unsigned char* plane, const float4 (&x)[8], float up) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float4 u = x[2 * w], v = x[2 * w + 1];
+            const float y[8] = {u.x * up, u.y * up, u.z * up, u.w * up, v.x * up, v.y * up, v.z * up, v.w * up};
+            rt_store_split<false>(plane, plane + kRtPlane, kr, kh * 4 + w, y);
+        }
+    };
+    float4 vf[KV4 ? 1 : 8];                        // f32: the next tile's V
+
+    // Gets tile c ready for its scores: looks it over, K into sK (every thread is done with the last
+    // tile's scores), f32's V into registers. True when something that a row sees is not finite: the
+    // tile is left to the plain loop. All threads return the same.
+    auto prepare = [&](int c, int pg) -> bool {
+        fac = 1.0f;
+        bool plain = false;
+        if constexpr (KV4) {
+            plain = survey4(c);
+            if (!plain) unpack_k4(c);
+            fence_async_smem();
+            __syncthreads();
+        } else {
+            // The powers of two stand while the values stay within 2^6 of the largest one met when they
+            // were set; a tile beyond them (the first one, to begin with) is measured by all threads.
+            float4 x[8];
+            load_f32(c, pg, a.k, x);
+            load_f32(c, pg, a.vv, vf);
+            uint32_t km = magnitude(x), vm = magnitude(vf);
+            const uint32_t klim = static_cast<uint32_t>(min(127 + ek + 6, 255)) << 23;
+            const uint32_t vlim = static_cast<uint32_t>(min(127 + E + 6, 255)) << 23;
+            bool over = c == c0 || km >= klim || vm >= vlim;
+            if (!over) store_f32(sK, x, pow2i(10 - ek));
+            fence_async_smem();
+            over = __syncthreads_or(over);
+            if (over) {
+                km = __reduce_max_sync(0xffffffffu, km);
+                vm = __reduce_max_sync(0xffffffffu, vm);
+                if (lane == 0) {
+                    sm_kmax[warp] = km;
+                    sm_vmax[warp] = vm;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    km = max(km, sm_kmax[w]);
+                    vm = max(vm, sm_vmax[w]);
+                }
+                plain = max(km, vm) >= 0x7f800000u;
+                if (!plain) {
+                    ek = max(ek, static_cast<int>(km >> 23) - 127);
+                    raise_E(static_cast<int>(vm >> 23) - 127);
+                    load_f32(c, pg, a.k, x);
+                    store_f32(sK, x, pow2i(10 - ek));
+                }
+                fence_async_smem();
+                __syncthreads();
+            }
+            bad = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) bad |= sm_bad[(c - c0) & 1][w] << w;
+        }
+        return plain;
+    };
+
+    if (KV4) cp_async_wait<0>();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * 64;
+    const uint32_t t_o = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128 + half * 32;
+    const float f_row = sm_f[row];
+    uint32_t ph_s = 0, ph_o = 0;                   // the barriers' phases
+    // S = Q K^T, low parts first
+    auto start_scores = [&]() {
+        if (tid != 0) return;
+        tc_fence_after();
+        constexpr uint32_t id = idesc_f16(kRtKeys, false);
+        const uint64_t qh = smem_desc_sw128(sQ), ql = smem_desc_sw128(sQ + kRtPlane), kd = smem_desc_sw128(sK);
+        if (!KV4) {
+            const uint64_t kl = smem_desc_sw128(sK + kRtPlane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) umma_f16_ss(tmem, qh + 2 * i, kl + 2 * i, id, i > 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) umma_f16_ss(tmem, ql + 2 * i, kd + 2 * i, id, !KV4 || i > 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) umma_f16_ss(tmem, qh + 2 * i, kd + 2 * i, id, 1);
+        umma_commit(&bar_s);
+    };
+    // V of tile c into sV; every thread has seen the last P V end.
+    auto store_v = [&](int c) {
+        if constexpr (KV4) unpack_v4(c); else store_f32(sV, vf, pow2i(10 - E));
+    };
+    bool plain = false;
+    if (c0 < c_end) {
+        plain = prepare(c0, page);
+        if (!plain) {
+            start_scores();
+            store_v(c0);
+        }
+    }
 
     for (int c = c0; c < c_end; ++c) {
-        const int buf = (c - c0) & 1;
         const int j0 = unit_chunk(k, c) * kRtKeys;
-        if (!KV4 && c > c0) {
-            load(c, page);
-            survey(c, page, buf);
-            __syncthreads();
-        }
-        uint32_t km = 0, vm = 0, nan = 0, bad = 0;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            km = max(km, sm_kmax[buf][w]);
-            vm = max(vm, sm_vmax[buf][w]);
-            nan |= sm_nan[buf][w];
-            bad |= sm_bad[buf][w] << w;
-        }
-        const int ek = max(static_cast<int>(km >> 23) - 127, -100);
-        const int ev = max(static_cast<int>(vm >> 23) - 127, -100);
-        const int E_new = max(E, ev);
-        const float fac = E < E_new - 120 ? 0.0f : pow2i(E - E_new);
-        E = E_new;
-
+        stage_tile(c + 1, page_next);
+        const int page_after = key_page(c + 2);
         // this row's keys: 32-column masks, unless every row sees the whole tile
         const bool full = bad == 0 && j0 + kRtKeys - 1 <= p_first && j0 + kRtKeys <= end &&
                           (a.window == 0 || j0 > p_last - a.window || j0 + kRtKeys <= a.sinks);
@@ -320,20 +479,82 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             const uint32_t miss = (bad >> (2 * b)) & 3u;
             return v & ~(((miss & 1u) ? 0xffffu : 0u) | ((miss & 2u) ? 0xffff0000u : 0u));
         };
+        float corr = 1.0f;
+        if (!plain) {
+            if (!mbar_wait_bounded(&bar_s, ph_s, nullptr)) s_fail = 1;
+            ph_s ^= 1u;
+            tc_fence_after();
 
-        if (nan) {
-            // ---- plain loop over the tile ----
-            float corr = 1.0f;
+            // ---- softmax ----
+            const float f = fmaxf(f_row * pow2i(ek - 10), 1.1754944e-38f);
+            float raw = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= fac;
+            for (int b = 0; b < 2; ++b) {
+                float x[32];
+                tmem_ld32(t_s + 32 * b, x);
+                if (full) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) raw = fmaxf(raw, x[i]);
+                } else {
+                    const uint32_t v = seen_bits(2 * half + b);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) raw = fmaxf(raw, (v >> i) & 1u ? x[i] : -INFINITY);
+                }
+            }
+            sm_x[half][row] = raw;
+            pair_sync(1 + (warp & 3));
+            raw = fmaxf(raw, sm_x[half ^ 1][row]);
+            const float mn = fmaxf(m, raw * f);
+            const bool far = !(fabsf(mn) < 65536.0f) && mn != -INFINITY;
+            const float ref = mn == -INFINITY ? 0.0f : far ? mn : mn - 12.0f;
+            corr = ex2(ref_old - ref);
+            m = mn;
+            ref_old = mn == -INFINITY ? -INFINITY : ref;
+            float2 sum = make_float2(0.0f, 0.0f);
+            // (far from 0, where f32 does not resolve 12, the product is rounded first, as the maximum's was)
+            const bool two_steps = __any_sync(0xffffffffu, far);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float x[16];
+                tmem_ld16(t_s + 16 * b, x);
+                if (two_steps) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = ex2(__fadd_rn(__fmul_rn(x[i], f), -ref));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 y = fma2(make_float2(x[i], x[i + 1]), make_float2(f, f), make_float2(-ref, -ref));
+                        x[i] = ex2(y.x);
+                        x[i + 1] = ex2(y.y);
+                    }
+                }
+                if (!full) {
+                    const uint32_t v = seen_bits(2 * half + (b >> 1)) >> ((b & 1) * 16);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = (v >> i) & 1u ? x[i] : 0.0f;
+                }
+                uint32_t p[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 y = make_float2(x[2 * i], x[2 * i + 1]);
+                    sum = add2(sum, y);
+                    const __half2 h = __floats2half2_rn(y.x, y.y);
+                    const float2 hf = __half22float2(h), r = fma2(hf, make_float2(-1.0f, -1.0f), y);
+                    p[i] = h2_bits(h);
+                    p[8 + i] = h2_bits(__floats2half2_rn(r.x, r.y));
+                }
+                tmem_st16(t_s + 16 * b, p);        // 8 columns of high parts, 8 of low parts
+            }
+            l = fmaf(l, corr, sum.x + sum.y);
+            tmem_st_wait();
+        } else {
+            // ---- plain loop over the tile ----
             const int ur = k.u0 + min(row, k.n_u - 1), h = hk * a.group + ur % a.group;
             const float* q = a.q + static_cast<long long>(s.row0 + ur / a.group) * a.q_ld + h * kHeadDim;
             const float vs = pow2i(vbits - E);
             for (int x = 0; x < kRtKeys; ++x) {
                 if (!((seen_bits(x >> 5) >> (x & 31)) & 1u)) continue;
-                const int j = j0 + x;
-                const int p = tab ? tab[j >> a.v.shift] : s.slot * a.v.pages_per_slot + (j >> a.v.shift);
-                const int pr = j & pr_mask;
+                const int j = j0 + x, p = page_of(j), pr = j & pr_mask;
                 float sc = 0.0f;
                 for (int d = 0; d < kHeadDim; d += 4) {
                     const float4 kv = rt_row4<KV4>(a, false, p, hk, pr, d);
@@ -343,11 +564,10 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
                 sc *= 0.125f * kLog2e;
                 const float mn = fmaxf(m, sc);
                 const float ref = mn == -INFINITY ? 0.0f : fabsf(mn) < 65536.0f ? mn - 12.0f : mn;
-                corr = ex2(ref_old - ref);
-                const float w = ex2(sc - ref);
+                const float cr = ex2(ref_old - ref), w = ex2(sc - ref);
                 m = mn;
                 ref_old = mn == -INFINITY ? -INFINITY : ref;
-                l = fmaf(l, corr, half == 0 ? w : 0.0f);
+                l = fmaf(l, cr, half == 0 ? w : 0.0f);
 #pragma unroll
                 for (int i4 = 0; i4 < 8; ++i4) {
                     const float4 v = rt_row4<KV4>(a, true, p, hk, pr, half * 32 + i4 * 4);
@@ -357,172 +577,57 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
                     for (int i = 0; i < 4; ++i) {
                         const float vi = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
                         float& oi = o[b0 + i * st];
-                        oi *= corr;
+                        oi *= cr;
                         if (w != 0.0f) oi = fmaf(w, vi * vs, oi);
                     }
                 }
             }
-            page = key_page(c + 1);
-            if (KV4) {
-                if (c + 1 < c_end) load(c + 1, page);
-                survey(c + 1, page, buf ^ 1);
-            }
-            __syncthreads();
-            continue;
         }
-
-        // ---- unpack the tile ----
-        if (KV4) {
-            // times 2^(10 - ek), and 16 times 2^(9 - E)
-            auto pair = [](uint32_t bits, float up) { return __float2half2_rn(__uint_as_float(bits) * up); };
-            const float ku = pow2i(10 - ek), vu = pow2i(13 - E);
-            const __half2 k0 = pair(ksw << 16, ku), k1 = pair(ksw & 0xffff0000u, ku);
-            const __half2 v0 = pair((kh ? vsw & 0xffff0000u : vsw << 16), vu), z0 = __hmul2(v0, __float2half2_rn(-1.5f));
-            const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
-            const __half2 sub = bits_h2(0x64086408u), s16 = bits_h2(0x2c002c00u), sub16 = bits_h2(0xd480d480u);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                // K: words 2 kh + w / 2 (+ 4 for odd w). 0x6400 | n is 1024 + n; a nibble four bits up
-                // gives 1024 + 16 n
-                const __half2 sc = (w & 1) ? k1 : k0;
-                const uint32_t x = kw[w], x8 = x >> 8;
-                uint4 r;
-                r.x = h2_bits(__hmul2(__hsub2(bits_h2((x & 0x000f000fu) | 0x64006400u), sub), sc));
-                r.y = h2_bits(__hmul2(__hfma2(bits_h2((x & 0x00f000f0u) | 0x64006400u), s16, sub16), sc));
-                r.z = h2_bits(__hmul2(__hsub2(bits_h2((x8 & 0x000f000fu) | 0x64006400u), sub), sc));
-                r.w = h2_bits(__hmul2(__hfma2(bits_h2((x8 & 0x00f000f0u) | 0x64006400u), s16, sub16), sc));
-                *rt_chunk(sK, kr, 2 * kh + (w >> 1) + 4 * (w & 1)) = r;
-                // V: words 4 kh + w, nibbles i and 4 + i of the halves: the order 0 4 1 5 2 6 3 7 again
-                uint32_t v[4];
-                kv4_values(vw[w], v0, z0, v);
-                *rt_chunk(sV, kr, 4 * kh + w) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-        } else {
-            const float ku = pow2i(10 - ek), vu = pow2i(10 - E);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                float x[8];
-                const float4 a0 = kf[2 * w], a1 = kf[2 * w + 1], b0 = vf[2 * w], b1 = vf[2 * w + 1];
-                x[0] = a0.x * ku, x[1] = a0.y * ku, x[2] = a0.z * ku, x[3] = a0.w * ku;
-                x[4] = a1.x * ku, x[5] = a1.y * ku, x[6] = a1.z * ku, x[7] = a1.w * ku;
-                rt_store_split<false>(sK, sK + kRtPlane, kr, kh * 4 + w, x);
-                x[0] = b0.x * vu, x[1] = b0.y * vu, x[2] = b0.z * vu, x[3] = b0.w * vu;
-                x[4] = b1.x * vu, x[5] = b1.y * vu, x[6] = b1.z * vu, x[7] = b1.w * vu;
-                rt_store_split<false>(sV, sV + kRtPlane, kr, kh * 4 + w, x);
-            }
-        }
-        fence_async_smem();
-        __syncthreads();
-        if (s_fail) break;                         // (uniform: set before a barrier, never cleared)
-
-        // ---- S = Q K^T: low parts first ----
-        if (tid == 0) {
-            tc_fence_after();
-            constexpr uint32_t id = idesc_f16(kRtKeys, false);
-            const uint64_t qh = smem_desc_sw128(sQ), ql = smem_desc_sw128(sQ + kRtPlane), kd = smem_desc_sw128(sK);
-            if (!KV4) {
-                const uint64_t kl = smem_desc_sw128(sK + kRtPlane);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) umma_f16_ss(tmem, qh + 2 * i, kl + 2 * i, id, i > 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) umma_f16_ss(tmem, ql + 2 * i, kd + 2 * i, id, !KV4 || i > 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) umma_f16_ss(tmem, qh + 2 * i, kd + 2 * i, id, 1);
-            umma_commit(&bar_s);
-        }
-        page = key_page(c + 1);
-        if (KV4 && c + 1 < c_end) load(c + 1, page);
-        if (!mbar_wait_bounded(&bar_s, ph, nullptr)) s_fail = 1;
-        tc_fence_after();
-
-        // ---- softmax ----
-        const float f = fmaxf(f_row * pow2i(ek - 10), 1.1754944e-38f);
-        float raw = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            float x[32];
-            tmem_ld32(t_s + 32 * b, x);
-            if (full) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) raw = fmaxf(raw, x[i]);
-            } else {
-                const uint32_t v = seen_bits(2 * half + b);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) raw = fmaxf(raw, (v >> i) & 1u ? x[i] : -INFINITY);
-            }
-        }
-        sm_x[half][row] = raw;
-        pair_sync(1 + (warp & 3));
-        raw = fmaxf(raw, sm_x[half ^ 1][row]);
-        const float mn = fmaxf(m, raw * f);
-        const bool far = !(fabsf(mn) < 65536.0f) && mn != -INFINITY;
-        const float ref = mn == -INFINITY ? 0.0f : far ? mn : mn - 12.0f;
-        const float corr = ex2(ref_old - ref);
-        m = mn;
-        ref_old = mn == -INFINITY ? -INFINITY : ref;
-        float sum = 0.0f;
-        // (far from 0, where f32 does not resolve 12, the product is rounded first, as the maximum's was)
-        const bool two_steps = __any_sync(0xffffffffu, far);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            float x[32];
-            tmem_ld32(t_s + 32 * b, x);
-            const uint32_t v = full ? 0xffffffffu : seen_bits(2 * half + b);
-            if (two_steps) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = ex2(__fadd_rn(__fmul_rn(x[i], f), -ref));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = ex2(fmaf(x[i], f, -ref));
-            }
-            if (!full) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = (v >> i) & 1u ? x[i] : 0.0f;
-            }
-            uint32_t p[32];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                sum += x[2 * i] + x[2 * i + 1];
-                split_f16(x[2 * i], x[2 * i + 1], p[i], p[16 + i]);
-            }
-            tmem_st32(t_s + 32 * b, p);            // 16 columns of high parts, 16 of low parts
-        }
-        l = fmaf(l, corr, sum);
-        tmem_st_wait();
-        if (KV4) survey(c + 1, page, buf ^ 1);
+        if (KV4) cp_async_wait<0>();
+        fence_async_smem();                        // V's unpacked values
         tc_fence_before();
         __syncthreads();
-
-        // ---- O = P V ----
-        if (tid == 0) {
+        if (s_fail) break;                         // (set before a barrier, never cleared)
+        if (!plain && tid == 0) {
+            // ---- O = P V ----
             tc_fence_after();
             constexpr uint32_t id = idesc_f16(kHeadDim, true);
             const uint64_t vd = smem_desc_sw128(sV), vl = smem_desc_sw128(sV + (KV4 ? 0 : kRtPlane));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)            // 16 keys: block i / 2 of 32, step i % 2; 2048 bytes of V
-                umma_f16_ts(tmem + 128, tmem + (i >> 1) * 32 + 16 + (i & 1) * 8, vd + 128 * i, id, i > 0);
+            for (int i = 0; i < 8; ++i)            // 16 keys: 8 + 8 columns of P, 2048 bytes of V
+                umma_f16_ts(tmem + 128, tmem + i * 16 + 8, vd + 128 * i, id, i > 0);
             if (!KV4) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    umma_f16_ts(tmem + 128, tmem + (i >> 1) * 32 + (i & 1) * 8, vl + 128 * i, id, 1);
+                    umma_f16_ts(tmem + 128, tmem + i * 16, vl + 128 * i, id, 1);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                umma_f16_ts(tmem + 128, tmem + (i >> 1) * 32 + (i & 1) * 8, vd + 128 * i, id, 1);
+                umma_f16_ts(tmem + 128, tmem + i * 16, vd + 128 * i, id, 1);
             umma_commit(&bar_o);
         }
-        if (!mbar_wait_bounded(&bar_o, ph, nullptr)) s_fail = 1;
-        ph ^= 1u;
-        tc_fence_after();
-        {
+        const bool running = !plain, more = c + 1 < c_end;
+        const float cf = corr * fac;               // (of this tile: preparing the next one may change fac)
+        plain = more && prepare(c + 1, page_next);
+        if (running) {
+            if (!mbar_wait_bounded(&bar_o, ph_o, nullptr)) s_fail = 1;
+            ph_o ^= 1u;
+            tc_fence_after();
+        }
+        if (more && !plain) start_scores();        // (over the columns that P V has read)
+        if (running) {
             float d[32];
             tmem_ld32(t_o, d);
-            const float cf = corr * fac;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = fmaf(o[i], cf, d[i]);
+            for (int i = 0; i < 32; i += 2) {
+                const float2 y = fma2(make_float2(o[i], o[i + 1]), make_float2(cf, cf), make_float2(d[i], d[i + 1]));
+                o[i] = y.x;
+                o[i + 1] = y.y;
+            }
+            tc_fence_before();
         }
-        tc_fence_before();
+        if (more && !plain) store_v(c + 1);
+        page_next = page_after;
     }
     // ---- finish ----
     __syncthreads();
@@ -540,10 +645,9 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         y[i] = (KV4 ? o[w * 8 + (d & 3) * 2 + (d >> 2)] : o[i]) * back;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float4 v = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-        store_unit_row(a, k, s, hk, sp, row, half * 8 + i, ref_old, L, v);
-    }
+    for (int i = 0; i < 8; ++i)
+        store_unit_row(a, k, s, hk, sp, row, half * 8 + i, ref_old, L,
+                       make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]));
 }
 
 }  // namespace dec

@@ -40,7 +40,7 @@ static int check_units() {
         a.window = (rnd() >> 8) % 3 ? static_cast<int>((rnd() >> 8) % 300) : 0;
         a.sinks = (rnd() >> 8) % 2 ? static_cast<int>((rnd() >> 8) % 90) : 0;
         a.S = 1 + static_cast<int>((rnd() >> 8) % 9);
-        a.min_chunks = 1 + static_cast<int>((rnd() >> 8) % 5);
+        a.per_split = 1 + static_cast<int>((rnd() >> 8) % 5);
         StreamRows s;
         s.row0 = 0;
         s.n = 1 + static_cast<int>((rnd() >> 8) % 70);
@@ -53,7 +53,7 @@ static int check_units() {
             CHECK(unit < units ? k.n_u >= 1 && k.n_u <= UR : k.n_u == 0);
             if (!k.n_u) continue;
             CHECK(k.splits >= 1 && k.splits <= a.S && k.end <= cap && k.total >= 0);
-            CHECK(k.total <= rows_max_chunks(a.v, s.n, a.window, a.sinks, CK));
+            CHECK(k.total <= rows_max_chunks(a.v, UR / a.group + 1, a.window, a.sinks, CK));
             CHECK(split_begin(k, 0) == 0 && split_begin(k, k.splits) == k.total);
             std::vector<int> seen(cap + CK, 0);
             for (int sp = 0; sp < k.splits; ++sp)

@@ -13,55 +13,58 @@ namespace {
 
 // Launch shape of a batch: unit rows per block, units per (stream, K/V head), splits per unit.
 struct RowsPlan {
-    int unit_rows, S, min_chunks;
+    int unit_rows, S, per_split;
     long long tiles;
     int most_splits;          // what the workspace is sized for
 };
 
-// Unit rows: the smallest variant that holds a stream's rows of one group; the largest one otherwise.
-// Splits: fewest (waves of resident blocks) x (rounds of chunks per warp, and one for the block's
-// start and end), a merge counting as one more; at most two waves of blocks, so that the workspace
-// does not depend on the window.
+// Unit rows: the smallest few-row variant that holds a stream's rows of one group; the tensor-core
+// tiles of 128 rows from where the widest few-row variant would need several units.
+//
+// Splits: the fewest (waves of resident blocks) x (rounds of chunks per block, and one for its start and
+// end), a merge counting as one more. Of the tensor-core splits within a tenth of the best the finest is
+// taken, and its length is fixed, so that blocks of short and long streams are alike. The workspace's
+// bound does not depend on the window.
 RowsPlan rows_plan(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, int n_heads, int window, int sinks) {
     RowsPlan p{};
-    const long long u = static_cast<long long>(rows.max_rows) * (n_heads / view.n_kv_heads);
-    int resident, warps, chunk;
-    // The tensor-core tiles of 128 rows pay from the second unit of the widest few-row variant on.
-    if (u > (kv4 ? 32 : 8)) {
+    const int group = n_heads / view.n_kv_heads;
+    const long long u = static_cast<long long>(rows.max_rows) * group;
+    const bool tc = u > (kv4 ? 32 : 8);
+    int resident, warps, chunk, least;
+    if (tc) {
         p.unit_rows = kRtRows;
-        resident = 2;
-        warps = 1;
-        chunk = kRtKeys;
-        p.min_chunks = 1;
+        resident = 2, warps = 1, chunk = kRtKeys, least = 1;
     } else if (kv4) {
         p.unit_rows = u <= 4 ? 4 : u <= 8 ? 8 : 16;
         resident = u <= 4 ? 4 : u <= 8 ? 3 : 2;
-        warps = kFewWarps;
-        chunk = kFewChunk;
-        p.min_chunks = kFewWarps;
+        warps = kFewWarps, chunk = kFewChunk, least = kFewWarps;
     } else {
         p.unit_rows = u <= 1 ? 1 : u <= 2 ? 2 : u <= 4 ? 4 : 8;
         resident = u <= 4 ? 4 : 3;
-        warps = kF32Warps;
-        chunk = kF32Chunk;
-        p.min_chunks = 2 * kF32Warps;
+        warps = kF32Warps, chunk = kF32Chunk, least = 2 * kF32Warps;
     }
     p.tiles = (u + p.unit_rows - 1) / p.unit_rows;
     const long long units = static_cast<long long>(rows.batch) * view.n_kv_heads * p.tiles;
     const long long slots = static_cast<long long>(kRowsSms) * resident;
     const KvViewDev v = view_dev(view);
-    const long long chunks = rows_max_chunks(v, rows.max_rows, window, sinks, chunk);
-    const long long cap = std::max(1ll, std::min<long long>(kRowsMaxSplits, (p.unit_rows == kRtRows ? 3 : 2) * slots / units));
-    p.most_splits = static_cast<int>(
-        std::max(1ll, std::min(cap, rows_max_chunks(v, rows.max_rows, 0, 0, chunk) / p.min_chunks)));
-    p.S = 1;
-    long long best = 0;
-    for (int S = 1; S <= p.most_splits && (S == 1 || chunks / S >= p.min_chunks); ++S) {
+    const long long span = std::min<long long>(rows.max_rows, p.unit_rows / group + 1);
+    const long long chunks = rows_max_chunks(v, span, window, sinks, chunk);
+    const long long all = rows_max_chunks(v, span, 0, 0, chunk);
+    p.most_splits = static_cast<int>(std::max(
+        1ll, std::min({static_cast<long long>(kRowsMaxSplits), (tc ? 8 : 2) * slots / units, all / least})));
+    auto cost = [&](long long S) {
         const long long rounds = ((chunks + S - 1) / S + warps - 1) / warps;
-        const long long cost = (units * S + slots - 1) / slots * (rounds + 1) + (S > 1);
-        if (S == 1 || cost < best) best = cost, p.S = S;
-        if (p.unit_rows == kRtRows) p.S = S;
-    }
+        return (units * S + slots - 1) / slots * (rounds + 1) + (S > 1);
+    };
+    const int most = static_cast<int>(std::max(1ll, std::min<long long>(p.most_splits, chunks / least)));
+    long long best = cost(1);
+    p.S = 1;
+    for (int S = 2; S <= most; ++S)
+        if (cost(S) < best) best = cost(S), p.S = S;
+    if (tc)
+        for (int S = most; S > p.S; --S)
+            if (10 * cost(S) <= 11 * best) p.S = S;
+    p.per_split = tc ? static_cast<int>((chunks + p.S - 1) / p.S) : least;
     return p;
 }
 
@@ -149,7 +152,7 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     a.out_ld = out_ld;
     a.part = static_cast<float*>(workspace);
     a.S = plan.S;
-    a.min_chunks = plan.min_chunks;
+    a.per_split = plan.per_split;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (plan.unit_rows == kRtRows)

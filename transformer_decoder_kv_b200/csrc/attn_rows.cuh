@@ -35,7 +35,7 @@ struct RowsAttnArgs {
     long long out_ld;
     float* part;                 // [n_rows * heads, S] partial states
     int S;                       // splits launched per unit
-    int min_chunks;              // fewest chunks worth a split
+    int per_split;               // chunks that make a split
 };
 
 // The keys of unit rows [u0, u0 + UR) of a stream in chunks of CK: chunks 0 .. sink_chunks - 1 and
@@ -74,7 +74,7 @@ __host__ __device__ __forceinline__ UnitKeys unit_keys(const RowsAttnArgs& a, co
     k.sink_chunks = sc;
     k.first = fc;
     k.total = sc + static_cast<int>((k.end + CK - 1) / CK) - fc;
-    const int most = k.total / a.min_chunks;
+    const int most = (k.total + a.per_split - 1) / a.per_split;
     k.splits = most < 1 ? 1 : (most < a.S ? most : a.S);
     return k;
 }
@@ -103,15 +103,15 @@ __device__ __forceinline__ void store_unit_row(const RowsAttnArgs& a, const Unit
     }
 }
 
-// Chunks of the widest unit, from the sizes the host knows.
-inline long long rows_max_chunks(const KvViewDev& v, int max_rows, int window, int sinks, int ck) {
+// Chunks (of ck) of the widest unit of at most `rows` query rows, from the sizes the host knows.
+inline long long rows_max_chunks(const KvViewDev& v, long long rows, int window, int sinks, int ck) {
     const long long cap = kv_capacity(v);
     long long keys = cap;
     if (window > 0) {
-        const long long seen = static_cast<long long>(window) + max_rows + ck;
+        const long long seen = static_cast<long long>(window) + rows + ck;
         keys = seen < cap ? seen : cap;
     }
-    long long extra = window > 0 && sinks > 0 ? (sinks < cap ? sinks : cap) : 0;
+    const long long extra = window > 0 && sinks > 0 ? (sinks < cap ? sinks : cap) : 0;
     const long long whole = (cap + ck - 1) / ck, c = (keys + ck - 1) / ck + (extra + ck - 1) / ck;
     return c < whole ? (c < 1 ? 1 : c) : whole;
 }

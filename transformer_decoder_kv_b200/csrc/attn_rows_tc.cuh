@@ -13,8 +13,10 @@
 //               tile's product is read back and added to the running f32 sums in registers, scaled by
 //               the change of the maximum, so that the tensor cores' truncation does not build up.
 //
-// A block (256 threads, two per SM) alternates between its softmax and the two products, and unpacks
-// the next tile's K while P V runs and its V while Q K^T runs; the other block of the SM fills the gaps.
+// A block (256 threads, two per SM) alternates between its softmax and the two products. The thread
+// that issues a product is held for as long as the product runs, so the warps share the rest: warp 0
+// issues P V while warps 4..7 unpack the next tile's K, then warp 4 issues Q K^T while warps 0..3 unpack
+// its V; the other block of the SM fills the gaps.
 // A 4-bit cache's tile is copied into shared memory by cp.async one tile ahead; an f32 tile goes
 // through registers. An M128 N128 K16 MMA takes 65 SM cycles and an M128 N64 K16 one 45 to 49
 // (measured), 1240 per tile of a 4-bit cache; the softmax, about 6 instructions per score and an exp2
@@ -165,7 +167,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     __shared__ uint32_t s_tmem;
     __shared__ float sm_f[kRtRows], sm_x[2][kRtRows];            // row factors; column halves' maxima, sums
     __shared__ uint32_t sm_bad[2][8];                            // of a tile's 16-key blocks: no page
-    __shared__ uint32_t sm_kmax[8], sm_vmax[8];                     // f32: magnitudes
+    __shared__ uint32_t sm_mag[8];                               // f32: magnitudes
     __shared__ int s_fail;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -192,35 +194,40 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         tmem_relinquish();
     }
 
-    // ---- keys: thread = key tid / 2 of a tile, half of its dims ----
-    const int kr = tid >> 1, kh = tid & 1;
+    // ---- keys ----
+    // a tile is fetched by thread = key kr (4-bit cache: and half kh of its codes), and unpacked by
+    // warps 4..7 (K) and 0..3 (V), thread = key ku
+    const int kr = KV4 ? tid >> 1 : tid & 127, kh = tid & 1, ku = tid & 127;
+    const bool k_side = warp >= 4;
     const int* tab = a.v.table ? a.v.table + s.slot * a.v.pages_per_slot : nullptr;
     const int pr_mask = a.v.shift == 31 ? 0x7fffffff : a.v.page_rows - 1;
-    auto page_of = [&](int j) {                    // of a key below `end`; -1: no page
-        const int p = tab ? tab[j >> a.v.shift] : s.slot * a.v.pages_per_slot + (j >> a.v.shift);
-        return static_cast<unsigned>(p) < static_cast<unsigned>(a.v.n_pages) ? p : -1;
-    };
+    // Table entry of a key below `end` (not yet checked: the value is first used a tile later), -1 beyond.
+    auto page_entry = [&](int j) { return tab ? tab[j >> a.v.shift] : s.slot * a.v.pages_per_slot + (j >> a.v.shift); };
+    auto checked = [&](int p) { return static_cast<unsigned>(p) < static_cast<unsigned>(a.v.n_pages) ? p : -1; };
     auto key_page = [&](int c) {
-        if (c >= c_end) return -1;
-        const int j = unit_chunk(k, c) * kRtKeys + kr;
-        return j < end ? page_of(j) : -1;
+        int p = -1;
+        if (c < c_end) {
+            const int j = unit_chunk(k, c) * kRtKeys + kr;
+            if (j < end) p = page_entry(j);
+        }
+        return p;
     };
     auto seen = [&](int j) { return j < end && (j >= seen_lo || j < a.sinks); };
     // Copies the tile into its stage (4-bit cache), and notes its blocks without a page.
-    auto stage_tile = [&](int c, int page) {
-        const int buf = (c - c0) & 1;
+    auto stage_tile = [&](int c, int entry) {
+        const int buf = (c - c0) & 1, pg = checked(entry);
         if (c < c_end) {
-            if (KV4 && page >= 0) {
+            if (KV4 && pg >= 0) {
                 const int pr = (unit_chunk(k, c) * kRtKeys + kr) & pr_mask;
                 const int part = a.v.page_rows * kKv4RowBytes;
-                const unsigned char* blk = a.cache + kv4_block(a.v, page, hk);
+                const unsigned char* blk = a.cache + kv4_block(a.v, pg, hk);
                 unsigned char* dst = stages + buf * kRtStage;
                 cp_async16(dst + tid * 16, blk + pr * 32 + kh * 16);
                 cp_async16(dst + kRtV + tid * 16, blk + part + pr * 32 + kh * 16);
                 if ((kr & 3) == 0)                 // four keys' scales of K, of V
                     cp_async16(dst + (kh ? kRtVs : kRtKs) + kr * 4, blk + kh * part + a.v.page_rows * 32 + pr * 4);
             }
-            if (lane == 0) sm_bad[buf][warp] = page < 0 && unit_chunk(k, c) * kRtKeys + kr < end;
+            if ((kr & 15) == 0) sm_bad[buf][kr >> 4] = pg < 0 && unit_chunk(k, c) * kRtKeys + kr < end;
         }
         if (KV4) cp_async_commit();
     };
@@ -231,10 +238,11 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
 
     // ---- queries: thread = row tid / 2, half of its dims ----
     {
+        const int qr = tid >> 1;
         float x[32];
         float mx = 0.0f;
-        if (kr < k.n_u) {
-            const int ur = k.u0 + kr, h = hk * a.group + ur % a.group;
+        if (qr < k.n_u) {
+            const int ur = k.u0 + qr, h = hk * a.group + ur % a.group;
             const float4* q = reinterpret_cast<const float4*>(a.q + static_cast<long long>(s.row0 + ur / a.group) * a.q_ld +
                                                               h * kHeadDim + kh * 32);
 #pragma unroll
@@ -255,8 +263,8 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] *= up;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) rt_store_split<KV4>(sQ, sQ + kRtPlane, kr, kh * 4 + w, x + 8 * w);
-        if (kh == 0) sm_f[kr] = pow2i(e - 10) * (0.125f * kLog2e);
+        for (int w = 0; w < 4; ++w) rt_store_split<KV4>(sQ, sQ + kRtPlane, qr, kh * 4 + w, x + 8 * w);
+        if (kh == 0) sm_f[qr] = pow2i(e - 10) * (0.125f * kLog2e);
     }
 
     // ---- rows: thread = row 32 (warp % 4) + lane, columns 64 half .. of S and 32 half .. of O ----
@@ -301,54 +309,60 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         return false;
     };
     auto live_key = [&](int c) {
-        return seen(unit_chunk(k, c) * kRtKeys + kr) && !((bad >> (kr >> 4)) & 1u);
+        return seen(unit_chunk(k, c) * kRtKeys + ku) && !((bad >> (ku >> 4)) & 1u);
     };
     // Unpacks K (times 2^(10 - ek)).
     auto unpack_k4 = [&](int c) {
         const unsigned char* st = stages + ((c - c0) & 1) * kRtStage;
-        const uint4 kc = *reinterpret_cast<const uint4*>(st + tid * 16);
-        const uint32_t ksw = live_key(c) ? *reinterpret_cast<const uint32_t*>(st + kRtKs + kr * 4) : 0u;
-        const float ku = pow2i(10 - ek);
-        const __half2 k0 = __float2half2_rn(__uint_as_float(ksw << 16) * ku);
-        const __half2 k1 = __float2half2_rn(__uint_as_float(ksw & 0xffff0000u) * ku);
-        const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w};
+        const uint32_t ksw = live_key(c) ? *reinterpret_cast<const uint32_t*>(st + kRtKs + ku * 4) : 0u;
+        const float up = pow2i(10 - ek);
+        const __half2 k0 = __float2half2_rn(__uint_as_float(ksw << 16) * up);
+        const __half2 k1 = __float2half2_rn(__uint_as_float(ksw & 0xffff0000u) * up);
         const __half2 sub = bits_h2(0x64086408u), s16 = bits_h2(0x2c002c00u), sub16 = bits_h2(0xd480d480u);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            // words 2 kh + w / 2 (+ 4 for odd w). 0x6400 | n is 1024 + n; a nibble four bits up gives
-            // 1024 + 16 n
-            const __half2 sc = (w & 1) ? k1 : k0;
-            const uint32_t x = kw[w], x8 = x >> 8;
-            uint4 r;
-            r.x = h2_bits(__hmul2(__hsub2(bits_h2((x & 0x000f000fu) | 0x64006400u), sub), sc));
-            r.y = h2_bits(__hmul2(__hfma2(bits_h2((x & 0x00f000f0u) | 0x64006400u), s16, sub16), sc));
-            r.z = h2_bits(__hmul2(__hsub2(bits_h2((x8 & 0x000f000fu) | 0x64006400u), sub), sc));
-            r.w = h2_bits(__hmul2(__hfma2(bits_h2((x8 & 0x00f000f0u) | 0x64006400u), s16, sub16), sc));
-            *rt_chunk(sK, kr, 2 * kh + (w >> 1) + 4 * (w & 1)) = r;
+        for (int hf = 0; hf < 2; ++hf) {
+            const uint4 kc = *reinterpret_cast<const uint4*>(st + ku * 32 + hf * 16);
+            const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                // words 2 hf + w / 2 (+ 4 for odd w). 0x6400 | n is 1024 + n; a nibble four bits up
+                // gives 1024 + 16 n
+                const __half2 sc = (w & 1) ? k1 : k0;
+                const uint32_t x = kw[w], x8 = x >> 8;
+                uint4 r;
+                r.x = h2_bits(__hmul2(__hsub2(bits_h2((x & 0x000f000fu) | 0x64006400u), sub), sc));
+                r.y = h2_bits(__hmul2(__hfma2(bits_h2((x & 0x00f000f0u) | 0x64006400u), s16, sub16), sc));
+                r.z = h2_bits(__hmul2(__hsub2(bits_h2((x8 & 0x000f000fu) | 0x64006400u), sub), sc));
+                r.w = h2_bits(__hmul2(__hfma2(bits_h2((x8 & 0x00f000f0u) | 0x64006400u), s16, sub16), sc));
+                *rt_chunk(sK, ku, 2 * hf + (w >> 1) + 4 * (w & 1)) = r;
+            }
         }
     };
     // Unpacks V (16 times the scale is 2^(13 - E) times it). A word's nibbles i and 4 + i come out
     // paired: the order 0 4 1 5 2 6 3 7 again.
     auto unpack_v4 = [&](int c) {
         const unsigned char* st = stages + ((c - c0) & 1) * kRtStage;
-        const uint4 vc = *reinterpret_cast<const uint4*>(st + kRtV + tid * 16);
-        const uint32_t vsw = live_key(c) ? *reinterpret_cast<const uint32_t*>(st + kRtVs + kr * 4) : 0u;
-        const __half2 v0 = __float2half2_rn(__uint_as_float(kh ? vsw & 0xffff0000u : vsw << 16) * pow2i(13 - E));
-        const __half2 z0 = __hmul2(v0, __float2half2_rn(-1.5f));
-        const uint32_t vw[4] = {vc.x, vc.y, vc.z, vc.w};
+        const uint32_t vsw = live_key(c) ? *reinterpret_cast<const uint32_t*>(st + kRtVs + ku * 4) : 0u;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            uint32_t v[4];
-            kv4_values(vw[w], v0, z0, v);
-            *rt_chunk(sV, kr, 4 * kh + w) = make_uint4(v[0], v[1], v[2], v[3]);
+        for (int hf = 0; hf < 2; ++hf) {
+            const uint4 vc = *reinterpret_cast<const uint4*>(st + kRtV + ku * 32 + hf * 16);
+            const __half2 v0 = __float2half2_rn(__uint_as_float(hf ? vsw & 0xffff0000u : vsw << 16) * pow2i(13 - E));
+            const __half2 z0 = __hmul2(v0, __float2half2_rn(-1.5f));
+            const uint32_t vw[4] = {vc.x, vc.y, vc.z, vc.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t v[4];
+                kv4_values(vw[w], v0, z0, v);
+                *rt_chunk(sV, ku, 4 * hf + w) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
         }
     };
-    // f32: this thread's 32 dims of K or V, 0 where no row sees the key.
-    auto load_f32 = [&](int c, int pg, const float* pool, float4 (&x)[8]) {
-        const int j = unit_chunk(k, c) * kRtKeys + kr;
+    // f32: half hf of key ku's dims, 0 where no row sees the key.
+    auto load_f32 = [&](int c, int entry, const float* pool, int hf, float4 (&x)[8]) {
+        const int j = unit_chunk(k, c) * kRtKeys + ku, pg = checked(entry);
         const bool live = pg >= 0 && seen(j);
         const float4* src = reinterpret_cast<const float4*>(
-            pool + (live ? kvf_block(a.v, pg, hk) + static_cast<long long>(j & pr_mask) * kHeadDim + kh * 32 : 0));
+            pool + (live ? kvf_block(a.v, pg, hk) + static_cast<long long>(j & pr_mask) * kHeadDim + hf * 32 : 0));
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = live ? __ldg(src + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     };
@@ -361,60 +375,64 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
                     max(__float_as_uint(fabsf(x[n].z)), __float_as_uint(fabsf(x[n].w))));
         return g;
     };
-    // f32: scales, splits and stores.
-    auto store_f32 = [&](unsigned char* plane, const float4 (&x)[8], float up) {
+    // f32: key ku's K or V scaled, split and stored; returns the largest magnitude.
+    auto copy_f32 = [&](int c, int entry, const float* pool, unsigned char* plane, float up) {
+        uint32_t g = 0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float4 u = x[2 * w], v = x[2 * w + 1];
-            const float y[8] = {u.x * up, u.y * up, u.z * up, u.w * up, v.x * up, v.y * up, v.z * up, v.w * up};
-            rt_store_split<false>(plane, plane + kRtPlane, kr, kh * 4 + w, y);
+        for (int hf = 0; hf < 2; ++hf) {
+            float4 x[8];
+            load_f32(c, entry, pool, hf, x);
+            g = max(g, magnitude(x));
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float4 u = x[2 * w], v = x[2 * w + 1];
+                const float y[8] = {u.x * up, u.y * up, u.z * up, u.w * up, v.x * up, v.y * up, v.z * up, v.w * up};
+                rt_store_split<false>(plane, plane + kRtPlane, ku, hf * 4 + w, y);
+            }
         }
+        return g;
     };
-    float4 vf[KV4 ? 1 : 8];                        // f32: the next tile's V
 
-    // Gets tile c ready for its scores: looks it over, K into sK (every thread is done with the last
-    // tile's scores), f32's V into registers. True when something that a row sees is not finite: the
-    // tile is left to the plain loop. All threads return the same.
-    auto prepare = [&](int c, int pg) -> bool {
+    // Gets tile c ready for its scores: looks it over, and K into sK by warps 4..7 (every thread is done
+    // with the last tile's scores). True when something that a row sees is not finite: the tile is left
+    // to the plain loop. All threads return the same.
+    auto prepare = [&](int c, int entry) -> bool {
         fac = 1.0f;
         bool plain = false;
         if constexpr (KV4) {
             plain = survey4(c);
-            if (!plain) unpack_k4(c);
+            if (!plain && k_side) unpack_k4(c);
             fence_async_smem();
             __syncthreads();
         } else {
             // The powers of two stand while the values stay within 2^6 of the largest one met when they
-            // were set; a tile beyond them (the first one, to begin with) is measured by all threads.
-            float4 x[8];
-            load_f32(c, pg, a.k, x);
-            load_f32(c, pg, a.vv, vf);
-            uint32_t km = magnitude(x), vm = magnitude(vf);
-            const uint32_t klim = static_cast<uint32_t>(min(127 + ek + 6, 255)) << 23;
-            const uint32_t vlim = static_cast<uint32_t>(min(127 + E + 6, 255)) << 23;
-            bool over = c == c0 || km >= klim || vm >= vlim;
-            if (!over) store_f32(sK, x, pow2i(10 - ek));
+            // were set; a tile beyond them (the first one, to begin with) sets them anew.
+            uint32_t mag;
+            if (k_side) {
+                mag = copy_f32(c, entry, a.k, sK, pow2i(10 - ek));
+            } else {
+                float4 x[8], y[8];
+                load_f32(c, entry, a.vv, 0, x);
+                load_f32(c, entry, a.vv, 1, y);
+                mag = max(magnitude(x), magnitude(y));
+            }
+            const uint32_t lim = static_cast<uint32_t>(min(127 + (k_side ? ek : E) + 6, 255)) << 23;
             fence_async_smem();
-            over = __syncthreads_or(over);
-            if (over) {
-                km = __reduce_max_sync(0xffffffffu, km);
-                vm = __reduce_max_sync(0xffffffffu, vm);
-                if (lane == 0) {
-                    sm_kmax[warp] = km;
-                    sm_vmax[warp] = vm;
-                }
+            if (__syncthreads_or(c == c0 || mag >= lim)) {
+                mag = __reduce_max_sync(0xffffffffu, mag);
+                if (lane == 0) sm_mag[warp] = mag;
                 __syncthreads();
+                uint32_t km = 0, vm = 0;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    km = max(km, sm_kmax[w]);
-                    vm = max(vm, sm_vmax[w]);
+                for (int w = 0; w < 4; ++w) {
+                    vm = max(vm, sm_mag[w]);
+                    km = max(km, sm_mag[4 + w]);
                 }
                 plain = max(km, vm) >= 0x7f800000u;
                 if (!plain) {
                     ek = max(ek, static_cast<int>(km >> 23) - 127);
                     raise_E(static_cast<int>(vm >> 23) - 127);
-                    load_f32(c, pg, a.k, x);
-                    store_f32(sK, x, pow2i(10 - ek));
+                    if (k_side) copy_f32(c, entry, a.k, sK, pow2i(10 - ek));
                 }
                 fence_async_smem();
                 __syncthreads();
@@ -435,9 +453,9 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     const uint32_t t_o = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128 + half * 32;
     const float f_row = sm_f[row];
     uint32_t ph_s = 0, ph_o = 0;                   // the barriers' phases
-    // S = Q K^T, low parts first
+    // S = Q K^T, low parts first (issued by warp 4)
     auto start_scores = [&]() {
-        if (tid != 0) return;
+        if (tid != 128) return;
         tc_fence_after();
         constexpr uint32_t id = idesc_f16(kRtKeys, false);
         const uint64_t qh = smem_desc_sw128(sQ), ql = smem_desc_sw128(sQ + kRtPlane), kd = smem_desc_sw128(sK);
@@ -452,16 +470,17 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         for (int i = 0; i < 4; ++i) umma_f16_ss(tmem, qh + 2 * i, kd + 2 * i, id, 1);
         umma_commit(&bar_s);
     };
-    // V of tile c into sV; every thread has seen the last P V end.
-    auto store_v = [&](int c) {
-        if constexpr (KV4) unpack_v4(c); else store_f32(sV, vf, pow2i(10 - E));
+    // V of tile c into sV by warps 0..3; every thread has seen the last P V end.
+    auto store_v = [&](int c, int entry) {
+        if (k_side) return;
+        if constexpr (KV4) unpack_v4(c); else copy_f32(c, entry, a.vv, sV, pow2i(10 - E));
     };
     bool plain = false;
     if (c0 < c_end) {
         plain = prepare(c0, page);
         if (!plain) {
             start_scores();
-            store_v(c0);
+            store_v(c0, page);
         }
     }
 
@@ -554,7 +573,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             const float vs = pow2i(vbits - E);
             for (int x = 0; x < kRtKeys; ++x) {
                 if (!((seen_bits(x >> 5) >> (x & 31)) & 1u)) continue;
-                const int j = j0 + x, p = page_of(j), pr = j & pr_mask;
+                const int j = j0 + x, p = page_entry(j), pr = j & pr_mask;
                 float sc = 0.0f;
                 for (int d = 0; d < kHeadDim; d += 4) {
                     const float4 kv = rt_row4<KV4>(a, false, p, hk, pr, d);
@@ -626,7 +645,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             }
             tc_fence_before();
         }
-        if (more && !plain) store_v(c + 1);
+        if (more && !plain) store_v(c + 1, page_next);
         page_next = page_after;
     }
     // ---- finish ----

@@ -386,14 +386,15 @@ def _device_array(name: str, a, dtype: str, least: int, device=None) -> Optional
     if a is None:
         return None
     if hasattr(a, "data_ptr"):
-        if str(a.dtype) != "torch." + dtype:
+        if a.dtype is not getattr(sys.modules["torch"], dtype):
             _einval(f"{name}: expected {dtype}, got {a.dtype}")
         if not a.is_contiguous():
             _einval(f"{name}: must be contiguous")
         if a.numel() < least:
             _einval(f"{name}: {a.numel()} elements, needs {least}")
-        if not a.is_cuda or (device is not None and a.device != device):
+        if a.device != device if device is not None else not a.is_cuda:
             _einval(f"{name}: must be on {device or 'a CUDA device'}, is on {a.device}")
+        return a.data_ptr()
     return _ptr(a)
 
 
@@ -420,6 +421,17 @@ def _row_buffer(name: str, a, n_rows: int, width: int, device=None):
     return a.data_ptr(), stride[0] if shape[0] > 1 else width
 
 
+def _rows_2d(name: str, a, rows, width: int):
+    """_row_buffer of the batch's rows, quickly for the usual [n_rows, width] tensor."""
+    torch = rows.torch
+    if torch is not None and type(a) is torch.Tensor:
+        shape, stride = a.shape, a.stride()
+        if (len(shape) == 2 and shape[1] == width and stride[1] == 1 and shape[0] >= rows.n_rows
+                and a.dtype is torch.float32 and a.device == rows.device):
+            return a.data_ptr(), stride[0] if shape[0] > 1 else width
+    return _row_buffer(name, a, rows.n_rows, width, rows.device)
+
+
 class KvView:
     """A K/V cache in caller memory (dec_kv_view): n_slots slots of pages_per_slot pages of
     page_rows rows and n_kv_heads heads, through an int32 page table on the device
@@ -432,6 +444,8 @@ class KvView:
         ptr = _device_array("table", table, "int32", n_slots * pages_per_slot)
         self.c = DecKvView(n_kv_heads, page_rows, pages_per_slot, n_slots, n_pages or n_slots * pages_per_slot, ptr)
         self.ref = C.byref(self.c)
+        self.kv4_bytes = int(lib().dec_kv4_bytes(self.ref))
+        self.width = n_kv_heads * 64
 
 
 class KvRows:
@@ -448,53 +462,48 @@ class KvRows:
                            _device_array("lens", lens, "int32", batch))
         self.n_rows = n_rows or batch
         self.ref = C.byref(self.c)
+        self.torch = sys.modules.get("torch") if self.device is not None else None
 
 
 def _same_device(view: KvView, rows: KvRows):
     """The page table and the batch are on one device, the one the kernels will run on."""
-    if view.device is not None and rows.device is not None and view.device != rows.device:
-        _einval(f"the page table is on {view.device}, the batch on {rows.device}")
-    if rows.device is not None:
-        torch = sys.modules.get("torch")
-        if torch is not None and rows.device.index != torch.cuda.current_device():
-            _einval(f"the batch is on {rows.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if rows.torch is not None:
+        if view.device is not None and view.device != rows.device:
+            _einval(f"the page table is on {view.device}, the batch on {rows.device}")
+        if rows.device.index != rows.torch.cuda.current_device():
+            _einval(f"the batch is on {rows.device}, the current device is cuda:{rows.torch.cuda.current_device()}")
 
 
 def kv4_bytes(view: KvView) -> int:
     """Bytes of a 4-bit cache pool for `view`."""
-    n = int(lib().dec_kv4_bytes(view.ref))
-    if n == 0:
+    if view.kv4_bytes == 0:
         _einval("dec_kv4_bytes: bad view")
-    return n
+    return view.kv4_bytes
 
 
 def kv4_write(view: KvView, rows: KvRows, k, v, cache, stream: int = 0):
     """Quantise and store the batch's K and V rows (f32 [n_rows, n_kv_heads * 64], any row stride)."""
-    _kv4_rows("dec_kv4_write", view, rows, k, v, cache, stream)
+    _same_device(view, rows)
+    kp, ld = _rows_2d("k", k, rows, view.width)
+    vp, ld_v = _rows_2d("v", v, rows, view.width)
+    if ld != ld_v:
+        _einval("dec_kv4_write: k and v have different row strides")
+    _raise_thread_error(lib().dec_kv4_write(view.ref, rows.ref, kp, vp, ld, _pool(view, rows, cache), stream))
 
 
 def kv4_read(view: KvView, rows: KvRows, cache, k_out, v_out, stream: int = 0):
     """Read the batch's rows back as f32."""
-    _kv4_rows("dec_kv4_read", view, rows, k_out, v_out, cache, stream)
-
-
-def _kv4_rows(name: str, view: KvView, rows: KvRows, k, v, cache, stream: int):
     _same_device(view, rows)
-    width = view.c.n_kv_heads * 64
-    kp, ld = _row_buffer("k", k, rows.n_rows, width, rows.device)
-    vp, ld_v = _row_buffer("v", v, rows.n_rows, width, rows.device)
+    kp, ld = _rows_2d("k_out", k_out, rows, view.width)
+    vp, ld_v = _rows_2d("v_out", v_out, rows, view.width)
     if ld != ld_v:
-        _einval(f"{name}: k and v have different row strides")
-    cp = _device_array("cache", cache, "uint8", _lib_bytes(view), rows.device)
-    if name == "dec_kv4_write":
-        st = lib().dec_kv4_write(view.ref, rows.ref, kp, vp, ld, cp, stream)
-    else:
-        st = lib().dec_kv4_read(view.ref, rows.ref, cp, kp, vp, ld, stream)
-    _raise_thread_error(st)
+        _einval("dec_kv4_read: k_out and v_out have different row strides")
+    _raise_thread_error(lib().dec_kv4_read(view.ref, rows.ref, _pool(view, rows, cache), kp, vp, ld, stream))
 
 
-def _lib_bytes(view: KvView) -> int:
-    return int(lib().dec_kv4_bytes(view.ref))
+def _pool(view: KvView, rows: KvRows, cache) -> Optional[int]:
+    """Pointer of a 4-bit cache pool (uint8, dec_kv4_bytes)."""
+    return _device_array("cache", cache, "uint8", view.kv4_bytes, rows.device)
 
 
 def attention_rows_workspace_size(view: KvView, rows: KvRows, n_heads: int) -> int:
@@ -510,19 +519,18 @@ def attention_kv4(view: KvView, rows: KvRows, q, cache, n_heads: int, out, works
     """Attention of the batch's query rows (f32 [n_rows, n_heads * 64]) over a 4-bit cache: each sees
     the keys up to its own position, the last `window` of them (0: all) and the first `sinks`."""
     _same_device(view, rows)
-    qp, q_ld = _row_buffer("q", q, rows.n_rows, n_heads * 64, rows.device)
-    op, o_ld = _row_buffer("out", out, rows.n_rows, n_heads * 64, rows.device)
-    cp = _device_array("cache", cache, "uint8", _lib_bytes(view), rows.device)
-    _raise_thread_error(lib().dec_attention_kv4(view.ref, rows.ref, qp, q_ld, n_heads, cp, window, sinks, op, o_ld,
-                                                _ptr(workspace), workspace_bytes, stream))
+    qp, q_ld = _rows_2d("q", q, rows, n_heads * 64)
+    op, o_ld = _rows_2d("out", out, rows, n_heads * 64)
+    _raise_thread_error(lib().dec_attention_kv4(view.ref, rows.ref, qp, q_ld, n_heads, _pool(view, rows, cache), window, sinks,
+                                                op, o_ld, _ptr(workspace), workspace_bytes, stream))
 
 
 def attention_window(view: KvView, rows: KvRows, q, k, v, n_heads: int, out, workspace, workspace_bytes: int,
                      window: int = 0, sinks: int = 0, stream: int = 0):
     """attention_kv4 over f32 caches k and v ([n_pages, n_kv_heads, page_rows, 64] each)."""
     _same_device(view, rows)
-    qp, q_ld = _row_buffer("q", q, rows.n_rows, n_heads * 64, rows.device)
-    op, o_ld = _row_buffer("out", out, rows.n_rows, n_heads * 64, rows.device)
+    qp, q_ld = _rows_2d("q", q, rows, n_heads * 64)
+    op, o_ld = _rows_2d("out", out, rows, n_heads * 64)
     least = view.c.n_pages * view.c.n_kv_heads * view.c.page_rows * 64
     kp = _device_array("k", k, "float32", least, rows.device)
     vp = _device_array("v", v, "float32", least, rows.device)

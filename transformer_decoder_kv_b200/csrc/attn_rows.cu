@@ -13,59 +13,72 @@ namespace {
 
 // Launch shape of a batch: unit rows per block, units per (stream, K/V head), splits per unit.
 struct RowsPlan {
-    int unit_rows, S, per_split;
-    long long tiles;
-    int most_splits;          // what the workspace is sized for
+    bool tc;
+    int unit_rows, resident, warps, chunk, least;    // blocks per SM; warps that share a block's chunks;
+                                                     // keys per chunk; fewest chunks worth a split
+    int group;
+    long long tiles, units;
+    int most_splits;                                 // what the workspace is sized for
+    int S, per_split;
 };
 
 // Unit rows: the smallest few-row variant that holds a stream's rows of one group; the tensor-core
-// tiles of 128 rows from where the widest few-row variant would need several units.
-//
-// Splits: the fewest (waves of resident blocks) x (rounds of chunks per block, and one for its start and
-// end), a merge counting as one more. Of the tensor-core splits within a tenth of the best the finest is
-// taken, and its length is fixed, so that blocks of short and long streams are alike. The workspace's
-// bound does not depend on the window.
-RowsPlan rows_plan(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, int n_heads, int window, int sinks) {
+// tiles of 128 rows from where the widest few-row variant would need several units. The bound on the
+// splits does not depend on the window.
+RowsPlan rows_shape(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, int n_heads) {
     RowsPlan p{};
-    const int group = n_heads / view.n_kv_heads;
-    const long long u = static_cast<long long>(rows.max_rows) * group;
-    const bool tc = u > (kv4 ? 32 : 8);
-    int resident, warps, chunk, least;
-    if (tc) {
+    p.group = n_heads / view.n_kv_heads;
+    const long long u = static_cast<long long>(rows.max_rows) * p.group;
+    p.tc = u > (kv4 ? 32 : 8);
+    if (p.tc) {
         p.unit_rows = kRtRows;
-        resident = 2, warps = 1, chunk = kRtKeys, least = 1;
+        p.resident = 2, p.warps = 1, p.chunk = kRtKeys, p.least = 1;
     } else if (kv4) {
         p.unit_rows = u <= 4 ? 4 : u <= 8 ? 8 : 16;
-        resident = u <= 4 ? 4 : u <= 8 ? 3 : 2;
-        warps = kFewWarps, chunk = kFewChunk, least = kFewWarps;
+        p.resident = u <= 4 ? 4 : u <= 8 ? 3 : 2;
+        p.warps = kFewWarps, p.chunk = kFewChunk, p.least = kFewWarps;
     } else {
         p.unit_rows = u <= 1 ? 1 : u <= 2 ? 2 : u <= 4 ? 4 : 8;
-        resident = u <= 4 ? 4 : 3;
-        warps = kF32Warps, chunk = kF32Chunk, least = 2 * kF32Warps;
+        p.resident = u <= 4 ? 4 : 3;
+        p.warps = kF32Warps, p.chunk = kF32Chunk, p.least = 2 * kF32Warps;
     }
     p.tiles = (u + p.unit_rows - 1) / p.unit_rows;
-    const long long units = static_cast<long long>(rows.batch) * view.n_kv_heads * p.tiles;
-    const long long slots = static_cast<long long>(kRowsSms) * resident;
-    const KvViewDev v = view_dev(view);
-    const long long span = std::min<long long>(rows.max_rows, p.unit_rows / group + 1);
-    const long long chunks = rows_max_chunks(v, span, window, sinks, chunk);
-    const long long all = rows_max_chunks(v, span, 0, 0, chunk);
+    p.units = static_cast<long long>(rows.batch) * view.n_kv_heads * p.tiles;
+    const long long slots = static_cast<long long>(kRowsSms) * p.resident;
+    const long long all = rows_max_chunks(view_dev(view), 1, 0, 0, p.chunk);
     p.most_splits = static_cast<int>(std::max(
-        1ll, std::min({static_cast<long long>(kRowsMaxSplits), (tc ? 8 : 2) * slots / units, all / least})));
-    auto cost = [&](long long S) {
-        const long long rounds = ((chunks + S - 1) / S + warps - 1) / warps;
-        return (units * S + slots - 1) / slots * (rounds + 1) + (S > 1);
+        1ll, std::min({static_cast<long long>(kRowsMaxSplits), (p.tc ? 8 : 2) * slots / p.units, all / p.least})));
+    return p;
+}
+
+// Splits: the fewest (waves of resident blocks) x (rounds of chunks per block, and its start and end),
+// a merge counting as one more round. Of the tensor-core splits within a tenth of the best the finest
+// is taken, and its length is fixed, so that blocks of short and long streams are alike.
+void rows_splits(RowsPlan& p, const dec_kv_view& view, const dec_kv_rows& rows, int window, int sinks) {
+    const long long span = std::min<long long>(rows.max_rows, p.unit_rows / p.group + 1);
+    const int chunks = static_cast<int>(rows_max_chunks(view_dev(view), span, window, sinks, p.chunk));
+    const int most = std::max(1, std::min(p.most_splits, chunks / p.least));
+    const unsigned slots = kRowsSms * p.resident, start = p.tc ? 2 : 1;
+    auto cost = [&](unsigned S) {
+        const unsigned rounds = ((chunks + S - 1) / S + p.warps - 1) / p.warps;
+        return (static_cast<unsigned long long>(p.units) * S + slots - 1) / slots * (rounds + start) + (S > 1);
     };
-    const int most = static_cast<int>(std::max(1ll, std::min<long long>(p.most_splits, chunks / least)));
-    long long best = cost(1);
     p.S = 1;
-    for (int S = 2; S <= most; ++S)
-        if (cost(S) < best) best = cost(S), p.S = S;
-    if (tc)
+    unsigned long long best = most > 1 ? cost(1) : 0;
+    for (int S = 2; S <= most; ++S) {
+        const unsigned long long c = cost(S);
+        if (c < best) best = c, p.S = S;
+    }
+    if (p.tc)
         for (int S = most; S > p.S; --S)
             if (10 * cost(S) <= 11 * best) p.S = S;
-    p.per_split = tc ? static_cast<int>((chunks + p.S - 1) / p.S) : least;
-    return p;
+    p.per_split = p.tc ? (chunks + p.S - 1) / p.S : p.least;
+}
+
+size_t rows_workspace(const RowsPlan& p, const dec_kv_rows& rows, int n_heads) {
+    return 256 + (p.most_splits > 1
+                      ? static_cast<size_t>(rows.n_rows) * n_heads * p.most_splits * kPartStride * sizeof(float)
+                      : 0);
 }
 
 template <typename K, typename... Args>
@@ -129,13 +142,14 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     if (!bad && !(aligned16(q) && aligned16(out) && aligned16(workspace) && aligned16(cache) && aligned16(k) &&
                   aligned16(v)))
         bad = "q, out, workspace and the caches must be 16-byte aligned";
-    if (!bad && workspace_bytes < dec_attention_rows_workspace_size(view, rows, n_heads)) bad = "workspace too small";
     RowsPlan plan{};
     if (!bad) {
-        plan = rows_plan(KV4, *view, *rows, n_heads, window, sinks);
+        plan = rows_shape(KV4, *view, *rows, n_heads);
+        if (workspace_bytes < rows_workspace(plan, *rows, n_heads)) bad = "workspace too small";
         if (plan.tiles * view->n_kv_heads > 65535) bad = "max_rows * n_heads is too large";
     }
     if (bad) return rows_fail(who, DEC_EINVAL, bad);
+    rows_splits(plan, *view, *rows, window, sinks);
     RowsAttnArgs a{};
     a.v = view_dev(*view);
     a.r = rows_dev(*rows);
@@ -175,9 +189,8 @@ extern "C" {
 
 size_t dec_attention_rows_workspace_size(const dec_kv_view* view, const dec_kv_rows* rows, int32_t n_heads) {
     if (view_problem(view, false) || rows_problem(rows) || n_heads < 1 || n_heads % view->n_kv_heads) return 0;
-    int S = 1;
-    for (int kv4 = 0; kv4 < 2; ++kv4) S = std::max(S, rows_plan(kv4 != 0, *view, *rows, n_heads, 0, 0).most_splits);
-    return 256 + (S > 1 ? static_cast<size_t>(rows->n_rows) * n_heads * S * kPartStride * sizeof(float) : 0);
+    return std::max(rows_workspace(rows_shape(false, *view, *rows, n_heads), *rows, n_heads),
+                    rows_workspace(rows_shape(true, *view, *rows, n_heads), *rows, n_heads));
 }
 
 dec_status dec_attention_kv4(const dec_kv_view* view, const dec_kv_rows* rows, const float* q, int64_t q_ld,

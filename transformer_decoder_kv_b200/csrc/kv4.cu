@@ -6,12 +6,15 @@
 // |x - c s| <= s / 2 holds whatever its rounding (a / s <= 7 (1 + 2^-8) rounds to 7), and bf16 keeps
 // f32's range. c s has 3 + 8 significant bits: exact in f32, and in f16 up to a power of two.
 //
-// The code is decided exactly: c0 = rint(x * (1 / s)) is within one of it, and e = x - c0 s is exact
-// in f32 (fma; c0 s has 11 significant bits and cancels x's leading ones; s >= 2^-126 keeps the last
-// bit of c0 s above the subnormal grid), so comparing e with +-s / 2 settles borders and ties.
+// The code is decided exactly: c0, the integer next to x * (1 / s) in f32, is within one of it, and
+// e = x - c0 s is exact in f32 (fma; c0 s has 11 significant bits and cancels x's leading ones;
+// s >= 2^-126 keeps the last bit of c0 s above the subnormal grid), so comparing e with +-s / 2 settles
+// borders and ties; only an element within rounding of a border needs more than the comparison.
 //
-// One lane takes 8 consecutive dims: 8 lanes are one (row, head) of K or V, 4 lanes one scale.
-// Bound by memory: 512 bytes read and 72 written per (row, K/V head), the reverse for reading back.
+// One lane takes 8 consecutive dims: 8 lanes are one (row, head) of K or V, 4 lanes one scale. Bound by
+// memory: 512 bytes read and 72 written per (row, K/V head), the reverse for reading back. A lane has
+// kTasks rows of K and V in flight (32 bytes each, one 256-bit access where the rows are 32-byte
+// aligned), and a code takes about 8 instructions.
 #include "kv_rows.cuh"
 
 using namespace dec;
@@ -19,81 +22,135 @@ using namespace dec;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kTasks = 2;                          // (row, head) pairs per 8 lanes
 
-__device__ __forceinline__ int kv4_code(float x, float s, float inv) {
-    float c = rintf(x * inv);
-    c = fminf(fmaxf(c, -7.0f), 7.0f);
-    const float e = fmaf(-c, s, x), h = 0.5f * s;
-    int ci = static_cast<int>(c);
-    if (e > h || (e == h && (ci & 1))) ci += 1;
-    if (e < -h || (e == -h && (ci & 1))) ci -= 1;
-    return min(max(ci, -7), 7);
+struct F8 {
+    float v[8];
+};
+// 32 bytes of a row; WIDE: 32-byte aligned.
+template <bool WIDE>
+__device__ __forceinline__ F8 load8(const float* p) {
+    F8 x;
+    if (WIDE) {
+        asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=f"(x.v[0]), "=f"(x.v[1]), "=f"(x.v[2]), "=f"(x.v[3]), "=f"(x.v[4]), "=f"(x.v[5]), "=f"(x.v[6]), "=f"(x.v[7])
+            : "l"(p));
+    } else {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        x.v[0] = a.x, x.v[1] = a.y, x.v[2] = a.z, x.v[3] = a.w, x.v[4] = b.x, x.v[5] = b.y, x.v[6] = b.z, x.v[7] = b.w;
+    }
+    return x;
+}
+template <bool WIDE>
+__device__ __forceinline__ void store8(float* p, const F8& x) {
+    if (WIDE) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x.v[0]), "f"(x.v[1]),
+                     "f"(x.v[2]), "f"(x.v[3]), "f"(x.v[4]), "f"(x.v[5]), "f"(x.v[6]), "f"(x.v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<float4*>(p)[0] = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(x.v[4], x.v[5], x.v[6], x.v[7]);
+    }
 }
 
-template <bool WRITE>
+// Word of 8 codes + 8 and the bf16 bits of their scale, the group's four lanes together.
+__device__ __forceinline__ uint32_t kv4_quantise(const F8& x, unsigned mask, uint32_t& scale) {
+    float a = 0.0f;
+    bool finite = true;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        a = fmaxf(a, fabsf(x.v[j]));
+        finite = finite && fabsf(x.v[j]) <= 3.402823466e38f;
+    }
+    if (!finite) a = INFINITY;
+    a = fmaxf(a, __shfl_xor_sync(mask, a, 1));
+    a = fmaxf(a, __shfl_xor_sync(mask, a, 2));
+    scale = 0x7fc0u;
+    if (!(a < INFINITY)) return 0x88888888u;
+    const uint32_t u = __float_as_uint(__fdiv_rn(a, 7.0f));
+    scale = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+    if (scale < 0x0080u) {
+        scale = 0;
+        return 0x88888888u;
+    }
+    const float s = __uint_as_float(scale << 16), inv = 1.0f / s, h = 0.5f * s;
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        // 1.5 2^23 + c: its low bits are c's (two's complement)
+        const float t = fmaf(x.v[j], inv, 12582912.0f), c = t - 12582912.0f;
+        const float e = fmaf(-c, s, x.v[j]);
+        uint32_t n = __float_as_uint(t);
+        if (fabsf(e) >= h) {
+            if (e > h || (e == h && (n & 1u))) n += 1;
+            if (e < -h || (e == -h && (n & 1u))) n -= 1;
+        }
+        w |= (n & 15u) << (4 * j);
+    }
+    return w ^ 0x88888888u;                        // (c + 8) & 15
+}
+
+template <bool WRITE, bool WIDE>
 __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const KvRowsDev r, float* __restrict__ k,
                                                        float* __restrict__ vv, long long ld,
                                                        unsigned char* __restrict__ cache) {
-    const int b = blockIdx.y;
-    const StreamRows s = stream_rows(r, v, b);
+    const StreamRows s = stream_rows(r, v, blockIdx.y);
     const int l8 = threadIdx.x & 7;
-    const long long task = static_cast<long long>(blockIdx.x) * (kThreads / 8) + (threadIdx.x >> 3);
-    // tasks: (row, head), head fastest; a group of 8 lanes leaves or stays together
-    const int i = static_cast<int>(task / v.heads), head = static_cast<int>(task % v.heads);
-    if (i >= s.n) return;
-    int page = 0, pr = 0;
-    const bool ok = kv_place(v, s, i, page, pr);
-    if (WRITE && !ok) return;
     const unsigned mask = 0xffu << (threadIdx.x & 24);
-    unsigned char* blk = cache + kv4_block(v, ok ? page : 0, head);
+    const int n_tasks = s.n * v.heads;             // (fits: checked on the host); head fastest
+    const int first = blockIdx.x * (kThreads / 8 * kTasks) + (threadIdx.x >> 3);
+    F8 x[kTasks][2];
+    float* src[kTasks][2];
+    unsigned char* blk[kTasks];                    // null: nothing to store, or zeros to read
+    int pr[kTasks];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        float4* x = reinterpret_cast<float4*>((which ? vv : k) + static_cast<long long>(s.row0 + i) * ld +
-                                              head * kHeadDim + l8 * 8);
-        unsigned char* part = blk + which * v.page_rows * kKv4RowBytes;
-        // K words sit in the order 0 4 1 5 2 6 3 7, so that one 8-byte load of the attention kernels
-        // gives 8 dims of each scale's group
-        const int word = which ? l8 : (l8 & 3) * 2 + (l8 >> 2);
-        uint32_t* codes = reinterpret_cast<uint32_t*>(part + pr * 32 + word * 4);
-        uint16_t* scale = reinterpret_cast<uint16_t*>(part + v.page_rows * 32 + pr * 4 + (l8 >> 2) * 2);
+    for (int i = 0; i < kTasks; ++i) {
+        const int task = first + i * (kThreads / 8);
+        blk[i] = nullptr;
+        src[i][0] = nullptr;
+        if (task >= n_tasks) continue;             // (8 lanes alike)
+        const int row = task / v.heads, head = task - row * v.heads;
+        int page = 0;
+        if (kv_place(v, s, row, page, pr[i])) blk[i] = cache + kv4_block(v, page, head);
+        if (WRITE && !blk[i]) continue;
+        const long long off = static_cast<long long>(s.row0 + row) * ld + head * kHeadDim + l8 * 8;
+        src[i][0] = k + off;
+        src[i][1] = vv + off;
         if (WRITE) {
-            const float4 x0 = x[0], x1 = x[1];
-            const float e[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-            float a = 0.0f;
-            bool finite = true;
+            x[i][0] = load8<WIDE>(src[i][0]);
+            x[i][1] = load8<WIDE>(src[i][1]);
+        }
+    }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                a = fmaxf(a, fabsf(e[j]));
-                finite = finite && fabsf(e[j]) <= 3.402823466e38f;
-            }
-            if (!finite) a = INFINITY;
-            a = fmaxf(a, __shfl_xor_sync(mask, a, 1));
-            a = fmaxf(a, __shfl_xor_sync(mask, a, 2));
-            uint32_t w = 0x88888888u, sb = 0x7fc0u;
-            if (a < INFINITY) {
-                const float q = __fdiv_rn(a, 7.0f);
-                const uint32_t u = __float_as_uint(q);
-                sb = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-                if (sb < 0x0080u) sb = 0;
-                if (sb) {
-                    const float sc = __uint_as_float(sb << 16), inv = 1.0f / sc;
-                    w = 0;
+    for (int i = 0; i < kTasks; ++i) {
+        if (!src[i][0]) continue;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w |= static_cast<uint32_t>(kv4_code(e[j], sc, inv) + 8) << (4 * j);
+        for (int which = 0; which < 2; ++which) {
+            unsigned char* part = blk[i] + which * v.page_rows * kKv4RowBytes;
+            // K words sit in the order 0 4 1 5 2 6 3 7, so that one 8-byte load of the attention kernels
+            // gives 8 dims of each scale's group; V's halves are kept rotated left by 2, as they unpack them
+            const int word = which ? l8 : (l8 & 3) * 2 + (l8 >> 2);
+            uint32_t* codes = reinterpret_cast<uint32_t*>(part + pr[i] * 32 + word * 4);
+            uint16_t* scale = reinterpret_cast<uint16_t*>(part + v.page_rows * 32 + pr[i] * 4 + (l8 >> 2) * 2);
+            if (WRITE) {
+                uint32_t sb;
+                const uint32_t w = kv4_quantise(x[i][which], mask, sb);
+                *codes = which ? ((w << 2) & 0xfffcfffcu) | ((w >> 14) & 0x00030003u) : w;
+                if ((l8 & 3) == 0) *scale = static_cast<uint16_t>(sb);
+            } else {
+                uint32_t w = 0;
+                float sc = 0.0f;
+                if (blk[i]) {
+                    w = *codes;
+                    sc = __uint_as_float(static_cast<uint32_t>(*scale) << 16);
+                    if (which) w = ((w >> 2) & 0x3fff3fffu) | ((w << 14) & 0xc000c000u);
                 }
-            }
-            // V's halves are kept rotated left by 2, as the attention kernels unpack them
-            *codes = which ? ((w << 2) & 0xfffcfffcu) | ((w >> 14) & 0x00030003u) : w;
-            if ((l8 & 3) == 0) *scale = static_cast<uint16_t>(sb);
-        } else {
-            float e[8];
-            uint32_t w = ok ? *codes : 0x88888888u;
-            if (which && ok) w = ((w >> 2) & 0x3fff3fffu) | ((w << 14) & 0xc000c000u);
-            const float sc = ok ? __uint_as_float(static_cast<uint32_t>(*scale) << 16) : 0.0f;
+                F8 y;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = sc * static_cast<float>(static_cast<int>((w >> (4 * j)) & 15u) - 8);
-            x[0] = make_float4(e[0], e[1], e[2], e[3]);
-            x[1] = make_float4(e[4], e[5], e[6], e[7]);
+                for (int j = 0; j < 8; ++j)
+                    y.v[j] = blk[i] ? sc * static_cast<float>(static_cast<int>((w >> (4 * j)) & 15u) - 8) : 0.0f;
+                store8<WIDE>(src[i][which], y);
+            }
         }
     }
 }
@@ -107,12 +164,14 @@ dec_status kv4_rows(const char* who, const dec_kv_view* view, const dec_kv_rows*
     if (!bad && (ld < static_cast<int64_t>(view->n_kv_heads) * kHeadDim || (ld & 3)))
         bad = "ld must be a multiple of 4 and at least n_kv_heads * 64";
     if (!bad && !(aligned16(k) && aligned16(v) && aligned16(cache))) bad = "k, v and cache must be 16-byte aligned";
+    const long long tasks = bad ? 0 : static_cast<long long>(rows->max_rows) * view->n_kv_heads;
+    if (tasks > 0x7fff0000ll) bad = "max_rows * n_kv_heads is too large";
     if (bad) return rows_fail(who, DEC_EINVAL, bad);
-    const long long tasks = static_cast<long long>(rows->max_rows) * view->n_kv_heads;
-    const long long blocks = (tasks + kThreads / 8 - 1) / (kThreads / 8);
-    if (blocks > 0x7fffffffll) return rows_fail(who, DEC_EINVAL, "max_rows * n_kv_heads is too large");
-    k_kv4_rows<WRITE><<<dim3(static_cast<unsigned>(blocks), rows->batch), kThreads, 0,
-                        static_cast<cudaStream_t>(stream)>>>(view_dev(*view), rows_dev(*rows), k, v, ld, cache);
+    const unsigned per_block = kThreads / 8 * kTasks;
+    const dim3 grid((static_cast<unsigned>(tasks) + per_block - 1) / per_block, rows->batch);
+    const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | static_cast<uintptr_t>(ld * 4)) & 31) == 0;
+    const auto kern = wide ? k_kv4_rows<WRITE, true> : k_kv4_rows<WRITE, false>;
+    kern<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(view_dev(*view), rows_dev(*rows), k, v, ld, cache);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return rows_cuda_fail(who, e, "k_kv4_rows launch");
     return DEC_OK;

@@ -56,13 +56,13 @@ __device__ __forceinline__ void store8(float* p, const F8& x) {
 // Word of 8 codes + 8 and the bf16 bits of their scale, the group's four lanes together.
 __device__ __forceinline__ uint32_t kv4_quantise(const F8& x, unsigned mask, uint32_t& scale) {
     float a = 0.0f;
-    bool finite = true;
+    float2 z = make_float2(0.0f, 0.0f);            // 0 while everything is finite
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        a = fmaxf(a, fabsf(x.v[j]));
-        finite = finite && fabsf(x.v[j]) <= 3.402823466e38f;
+    for (int j = 0; j < 8; j += 2) {
+        a = fmaxf(a, fmaxf(fabsf(x.v[j]), fabsf(x.v[j + 1])));
+        z = fma2(make_float2(x.v[j], x.v[j + 1]), make_float2(0.0f, 0.0f), z);
     }
-    if (!finite) a = INFINITY;
+    if (!(z.x + z.y == 0.0f)) a = INFINITY;
     a = fmaxf(a, __shfl_xor_sync(mask, a, 1));
     a = fmaxf(a, __shfl_xor_sync(mask, a, 2));
     scale = 0x7fc0u;
@@ -74,20 +74,59 @@ __device__ __forceinline__ uint32_t kv4_quantise(const F8& x, unsigned mask, uin
         return 0x88888888u;
     }
     const float s = __uint_as_float(scale << 16), inv = 1.0f / s, h = 0.5f * s;
-    uint32_t w = 0;
+    // t = 1.5 2^23 + c: its low bits are c's (two's complement)
+    constexpr float kMagic = 12582912.0f;
+    uint32_t n[8];
+    float e[8], far = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        // 1.5 2^23 + c: its low bits are c's (two's complement)
-        const float t = fmaf(x.v[j], inv, 12582912.0f), c = t - 12582912.0f;
-        const float e = fmaf(-c, s, x.v[j]);
-        uint32_t n = __float_as_uint(t);
-        if (fabsf(e) >= h) {
-            if (e > h || (e == h && (n & 1u))) n += 1;
-            if (e < -h || (e == -h && (n & 1u))) n -= 1;
-        }
-        w |= (n & 15u) << (4 * j);
+    for (int j = 0; j < 8; j += 2) {
+        const float2 v = make_float2(x.v[j], x.v[j + 1]);
+        const float2 t = fma2(v, make_float2(inv, inv), make_float2(kMagic, kMagic));
+        const float2 c = add2(t, make_float2(-kMagic, -kMagic));
+        const float2 r = fma2(c, make_float2(-s, -s), v);
+        n[j] = __float_as_uint(t.x), n[j + 1] = __float_as_uint(t.y);
+        e[j] = r.x, e[j + 1] = r.y;
+        far = fmaxf(far, fmaxf(fabsf(r.x), fabsf(r.y)));
     }
+    if (far >= h) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t odd = n[j] & 1u;
+            if (e[j] > h || (e[j] == h && odd)) n[j] += 1;
+            if (e[j] < -h || (e[j] == -h && odd)) n[j] -= 1;
+        }
+    }
+    // two codes to a byte, four bytes to the word
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t hi = n[2 * j + 1] * 16u;
+        b[j] = (n[2 * j] & 15u) | (hi & ~15u);
+    }
+    const uint32_t w = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
     return w ^ 0x88888888u;                        // (c + 8) & 15
+}
+
+// The values of 8 codes + 8 of one scale. A nibble masked out at bit 8 (or 12) under the exponent of
+// 2^15 (2^11) is 2^15 + n (2^11 + n); one fma takes it to (n - 8) s, exactly: 2^15 + 8 times the scale's 8
+// significant bits has 21. Scales whose product with it would leave f32 go the long way.
+__device__ __forceinline__ F8 kv4_dequantise(uint32_t w, float s) {
+    F8 y;
+    if (s >= 1e30f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y.v[j] = s * static_cast<float>(static_cast<int>((w >> (4 * j)) & 15u) - 8);
+        return y;
+    }
+    const float2 c = make_float2(-32776.0f * s, -2056.0f * s);
+    const uint32_t x[4] = {w << 8, w, w >> 8, w >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = fma2(make_float2(__uint_as_float((x[i] & 0x00000f00u) | 0x47000000u),
+                                          __uint_as_float((x[i] & 0x0000f000u) | 0x45000000u)),
+                              make_float2(s, s), c);
+        y.v[2 * i] = v.x, y.v[2 * i + 1] = v.y;
+    }
+    return y;
 }
 
 template <bool WRITE, bool WIDE>
@@ -145,11 +184,8 @@ __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const 
                     sc = __uint_as_float(static_cast<uint32_t>(*scale) << 16);
                     if (which) w = ((w >> 2) & 0x3fff3fffu) | ((w << 14) & 0xc000c000u);
                 }
-                F8 y;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    y.v[j] = blk[i] ? sc * static_cast<float>(static_cast<int>((w >> (4 * j)) & 15u) - 8) : 0.0f;
-                store8<WIDE>(src[i][which], y);
+                // (a row without a place: scale 0 gives zeros)
+                store8<WIDE>(src[i][which], kv4_dequantise(w, sc));
             }
         }
     }

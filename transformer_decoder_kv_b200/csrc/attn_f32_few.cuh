@@ -28,6 +28,7 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_few(const Ro
     __shared__ __align__(16) float sm_o[kF32Warps][R][kHeadDim];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, d4 = lane & 15;
+    pdl_wait();
     const StreamRows s = stream_rows(a.r, a.v, blockIdx.z);
     const int n_tiles = gridDim.y / a.v.heads;
     const int hk = blockIdx.y / n_tiles;

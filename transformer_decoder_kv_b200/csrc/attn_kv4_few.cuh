@@ -118,6 +118,7 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
     __shared__ __align__(8) uint32_t sm_vs[kFewWarps][2][kFewChunk / 2];      // V scales of a chunk, f16, by group
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    pdl_wait();
     const StreamRows s = stream_rows(a.r, a.v, blockIdx.z);
     const int n_tiles = gridDim.y / a.v.heads;
     const int hk = blockIdx.y / n_tiles;

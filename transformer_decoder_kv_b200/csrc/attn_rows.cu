@@ -81,48 +81,37 @@ size_t rows_workspace(const RowsPlan& p, const dec_kv_rows& rows, int n_heads) {
                       : 0);
 }
 
-template <typename K, typename... Args>
-cudaError_t launch_after(K kern, dim3 grid, dim3 block, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
+template <int UR, int CK>
+cudaError_t launch_merge(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
+    if (p.S == 1) return cudaSuccess;
+    return rows_launch(k_attn_merge<UR, CK>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), 128, 0, st, a);
+}
+
+template <typename K>
+cudaError_t launch_units(K kern, const RowsAttnArgs& a, const RowsPlan& p, int threads, size_t smem, cudaStream_t st) {
+    return rows_launch(kern, dim3(p.S, static_cast<unsigned>(a.v.heads * p.tiles), a.r.batch), threads, smem, st, a);
 }
 
 template <int NT, bool PAIR>
 cudaError_t launch_kv4_few(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
     constexpr int UR = PAIR ? 4 : 8 * NT;
     static_assert(kFewWarps * kFewStages * kFewStageBytes <= 48 * 1024, "no opt-in needed");
-    k_attn_kv4_few<NT, PAIR><<<dim3(p.S, static_cast<unsigned>(a.v.heads * p.tiles), a.r.batch), kFewWarps * 32, few_smem_bytes(UR), st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.S == 1) return e;
-    return launch_after(k_attn_merge<UR, kFewChunk>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), dim3(128), st, a);
+    const cudaError_t e = launch_units(k_attn_kv4_few<NT, PAIR>, a, p, kFewWarps * 32, few_smem_bytes(UR), st);
+    return e == cudaSuccess ? launch_merge<UR, kFewChunk>(a, p, st) : e;
 }
 
 template <bool KV4>
 cudaError_t launch_rows_tc(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
     thread_local int attr_dev = -1;
     cudaError_t e = prefer_max_shared_once(k_attn_rows_tc<KV4>, attr_dev, rt_smem_bytes<KV4>());
-    if (e != cudaSuccess) return e;
-    k_attn_rows_tc<KV4><<<dim3(p.S, static_cast<unsigned>(a.v.heads * p.tiles), a.r.batch), kRtThreads, rt_smem_bytes<KV4>(), st>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || p.S == 1) return e;
-    return launch_after(k_attn_merge<kRtRows, kRtKeys>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), dim3(128), st,
-                        a);
+    if (e == cudaSuccess) e = launch_units(k_attn_rows_tc<KV4>, a, p, kRtThreads, rt_smem_bytes<KV4>(), st);
+    return e == cudaSuccess ? launch_merge<kRtRows, kRtKeys>(a, p, st) : e;
 }
 
 template <int R>
 cudaError_t launch_f32_few(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
-    k_attn_f32_few<R><<<dim3(p.S, static_cast<unsigned>(a.v.heads * p.tiles), a.r.batch), kF32Warps * 32, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.S == 1) return e;
-    return launch_after(k_attn_merge<R, kF32Chunk>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), dim3(128), st, a);
+    const cudaError_t e = launch_units(k_attn_f32_few<R>, a, p, kF32Warps * 32, 0, st);
+    return e == cudaSuccess ? launch_merge<R, kF32Chunk>(a, p, st) : e;
 }
 
 template <bool KV4>

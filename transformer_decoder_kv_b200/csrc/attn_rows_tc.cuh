@@ -154,6 +154,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     __shared__ int s_fail;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();
     const StreamRows s = stream_rows(a.r, a.v, blockIdx.z);
     const int n_tiles = gridDim.y / a.v.heads;
     const int hk = blockIdx.y / n_tiles;

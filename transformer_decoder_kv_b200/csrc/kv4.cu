@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTasks = 2;                          // (row, head) pairs per 8 lanes
+constexpr int kGroups = kThreads / 8 * kTasks;     // (row, head) pairs per block
 
 struct F8 {
     float v[8];
@@ -129,30 +130,44 @@ __device__ __forceinline__ F8 kv4_dequantise(uint32_t w, float s) {
     return y;
 }
 
+// A block's tile: 2^lh heads x 64 / 2^lh rows, so that a lane group finds its row and head by shifts
+// and several heads share a row's place. lh: the largest power of two (up to 16) that divides the
+// heads; no lane group is left without a head.
 template <bool WRITE, bool WIDE>
 __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const KvRowsDev r, float* __restrict__ k,
                                                        float* __restrict__ vv, long long ld,
-                                                       unsigned char* __restrict__ cache) {
+                                                       unsigned char* __restrict__ cache, int lh) {
+    pdl_wait();
     const StreamRows s = stream_rows(r, v, blockIdx.y);
+    const int head_blocks = v.heads >> lh, row_block = blockIdx.x / head_blocks;
+    const int head_block = blockIdx.x - row_block * head_blocks;
+    const int row0 = row_block * (kGroups >> lh);
+    if (row0 >= s.n) return;
     const int l8 = threadIdx.x & 7;
     const unsigned mask = 0xffu << (threadIdx.x & 24);
-    const int n_tasks = s.n * v.heads;             // (fits: checked on the host); head fastest
-    const int first = blockIdx.x * (kThreads / 8 * kTasks) + (threadIdx.x >> 3);
+    const int part = v.page_rows * kKv4RowBytes;
+    const unsigned page_bytes = static_cast<unsigned>(v.heads) * 2u * part;
+    const long long cap = kv_capacity(v);
     F8 x[kTasks][2];
-    float* src[kTasks][2];
-    unsigned char* blk[kTasks];                    // null: nothing to store, or zeros to read
+    float* src[kTasks][2];                         // null: no such row
+    unsigned char* blk[kTasks];                    // null: no place, nothing to store or zeros to read
     int pr[kTasks];
 #pragma unroll
     for (int i = 0; i < kTasks; ++i) {
-        const int task = first + i * (kThreads / 8);
+        const int g = (threadIdx.x >> 3) + i * (kThreads / 8);
+        const int row = row0 + (g >> lh), head = (head_block << lh) + (g & ((1 << lh) - 1));
         blk[i] = nullptr;
         src[i][0] = nullptr;
-        if (task >= n_tasks) continue;             // (8 lanes alike)
-        const int row = task / v.heads, head = task - row * v.heads;
-        int page = 0;
-        if (kv_place(v, s, row, page, pr[i])) blk[i] = cache + kv4_block(v, page, head);
+        if (row >= s.n) continue;                  // (8 lanes alike)
+        const long long pos = s.pos0 + row;
+        if (s.slot >= 0 && pos >= 0 && pos < cap) {
+            const int page = kv_page(v, s.slot, static_cast<int>(pos) >> v.shift);
+            pr[i] = static_cast<int>(pos) & (v.page_rows - 1);
+            if (page >= 0)
+                blk[i] = cache + static_cast<unsigned long long>(static_cast<unsigned>(page)) * page_bytes + head * (2 * part);
+        }
         if (WRITE && !blk[i]) continue;
-        const long long off = static_cast<long long>(s.row0 + row) * ld + head * kHeadDim + l8 * 8;
+        const long long off = static_cast<long long>(s.row0 + row) * ld + (head * kHeadDim + l8 * 8);
         src[i][0] = k + off;
         src[i][1] = vv + off;
         if (WRITE) {
@@ -160,33 +175,43 @@ __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const 
             x[i][1] = load8<WIDE>(src[i][1]);
         }
     }
+    // K words sit in the order 0 4 1 5 2 6 3 7, so that one 8-byte load of the attention kernels gives 8
+    // dims of each scale's group; V's halves are kept rotated left by 2, as they unpack them
+    const int kw = ((l8 & 3) * 2 + (l8 >> 2)) * 4, vw = part + l8 * 4, sw = v.page_rows * 32 + (l8 >> 2) * 2;
+    if (WRITE) {
 #pragma unroll
-    for (int i = 0; i < kTasks; ++i) {
-        if (!src[i][0]) continue;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            unsigned char* part = blk[i] + which * v.page_rows * kKv4RowBytes;
-            // K words sit in the order 0 4 1 5 2 6 3 7, so that one 8-byte load of the attention kernels
-            // gives 8 dims of each scale's group; V's halves are kept rotated left by 2, as they unpack them
-            const int word = which ? l8 : (l8 & 3) * 2 + (l8 >> 2);
-            uint32_t* codes = reinterpret_cast<uint32_t*>(part + pr[i] * 32 + word * 4);
-            uint16_t* scale = reinterpret_cast<uint16_t*>(part + v.page_rows * 32 + pr[i] * 4 + (l8 >> 2) * 2);
-            if (WRITE) {
-                uint32_t sb;
-                const uint32_t w = kv4_quantise(x[i][which], mask, sb);
-                *codes = which ? ((w << 2) & 0xfffcfffcu) | ((w >> 14) & 0x00030003u) : w;
-                if ((l8 & 3) == 0) *scale = static_cast<uint16_t>(sb);
-            } else {
-                uint32_t w = 0;
-                float sc = 0.0f;
-                if (blk[i]) {
-                    w = *codes;
-                    sc = __uint_as_float(static_cast<uint32_t>(*scale) << 16);
-                    if (which) w = ((w >> 2) & 0x3fff3fffu) | ((w << 14) & 0xc000c000u);
-                }
-                // (a row without a place: scale 0 gives zeros)
-                store8<WIDE>(src[i][which], kv4_dequantise(w, sc));
+        for (int i = 0; i < kTasks; ++i) {
+            if (!src[i][0]) continue;
+            unsigned char* codes = blk[i] + pr[i] * 32;
+            unsigned char* scale = blk[i] + sw + pr[i] * 4;
+            uint32_t sk, sv;
+            *reinterpret_cast<uint32_t*>(codes + kw) = kv4_quantise(x[i][0], mask, sk);
+            const uint32_t w = kv4_quantise(x[i][1], mask, sv);
+            *reinterpret_cast<uint32_t*>(codes + vw) = ((w << 2) & 0xfffcfffcu) | ((w >> 14) & 0x00030003u);
+            if ((l8 & 3) == 0) {
+                *reinterpret_cast<uint16_t*>(scale) = static_cast<uint16_t>(sk);
+                *reinterpret_cast<uint16_t*>(scale + part) = static_cast<uint16_t>(sv);
             }
+        }
+    } else {
+        uint32_t w[kTasks][2], sc[kTasks][2];
+#pragma unroll
+        for (int i = 0; i < kTasks; ++i) {
+            w[i][0] = w[i][1] = sc[i][0] = sc[i][1] = 0;       // (a row without a place: scale 0 gives zeros)
+            if (!blk[i]) continue;
+            const unsigned char* codes = blk[i] + pr[i] * 32;
+            const unsigned char* scale = blk[i] + sw + pr[i] * 4;
+            w[i][0] = *reinterpret_cast<const uint32_t*>(codes + kw);
+            w[i][1] = *reinterpret_cast<const uint32_t*>(codes + vw);
+            sc[i][0] = *reinterpret_cast<const uint16_t*>(scale);
+            sc[i][1] = *reinterpret_cast<const uint16_t*>(scale + part);
+        }
+#pragma unroll
+        for (int i = 0; i < kTasks; ++i) {
+            if (!src[i][0]) continue;
+            store8<WIDE>(src[i][0], kv4_dequantise(w[i][0], __uint_as_float(sc[i][0] << 16)));
+            const uint32_t y = ((w[i][1] >> 2) & 0x3fff3fffu) | ((w[i][1] << 14) & 0xc000c000u);
+            store8<WIDE>(src[i][1], kv4_dequantise(y, __uint_as_float(sc[i][1] << 16)));
         }
     }
 }
@@ -200,15 +225,17 @@ dec_status kv4_rows(const char* who, const dec_kv_view* view, const dec_kv_rows*
     if (!bad && (ld < static_cast<int64_t>(view->n_kv_heads) * kHeadDim || (ld & 3)))
         bad = "ld must be a multiple of 4 and at least n_kv_heads * 64";
     if (!bad && !(aligned16(k) && aligned16(v) && aligned16(cache))) bad = "k, v and cache must be 16-byte aligned";
-    const long long tasks = bad ? 0 : static_cast<long long>(rows->max_rows) * view->n_kv_heads;
-    if (tasks > 0x7fff0000ll) bad = "max_rows * n_kv_heads is too large";
     if (bad) return rows_fail(who, DEC_EINVAL, bad);
-    const unsigned per_block = kThreads / 8 * kTasks;
-    const dim3 grid((static_cast<unsigned>(tasks) + per_block - 1) / per_block, rows->batch);
+    int lh = 0;
+    while (lh < 4 && view->n_kv_heads % (2 << lh) == 0) ++lh;
+    const long long rows_per = kGroups >> lh;
+    const long long blocks = (rows->max_rows + rows_per - 1) / rows_per * (view->n_kv_heads >> lh);
+    if (blocks > 0x7fffffffll) return rows_fail(who, DEC_EINVAL, "max_rows * n_kv_heads is too large");
     const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | static_cast<uintptr_t>(ld * 4)) & 31) == 0;
-    const auto kern = wide ? k_kv4_rows<WRITE, true> : k_kv4_rows<WRITE, false>;
-    kern<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(view_dev(*view), rows_dev(*rows), k, v, ld, cache);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = rows_launch(wide ? k_kv4_rows<WRITE, true> : k_kv4_rows<WRITE, false>,
+                                      dim3(static_cast<unsigned>(blocks), rows->batch), kThreads, 0,
+                                      static_cast<cudaStream_t>(stream), view_dev(*view), rows_dev(*rows), k, v,
+                                      static_cast<long long>(ld), cache, lh);
     if (e != cudaSuccess) return rows_cuda_fail(who, e, "k_kv4_rows launch");
     return DEC_OK;
 }

@@ -157,6 +157,23 @@ inline KvRowsDev rows_dev(const dec_kv_rows& r) {
     return KvRowsDev{r.batch, r.n_rows, r.max_rows, r.row_start, r.slots, r.lens};
 }
 
+// Launch whose blocks may be set up while the kernel before them on the stream ends; each kernel
+// waits for it (griddepcontrol) before it reads anything.
+template <typename... P, typename... Args>
+cudaError_t rows_launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace dec

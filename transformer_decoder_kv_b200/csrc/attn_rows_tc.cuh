@@ -216,8 +216,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         if (KV4) cp_async_commit();
     };
 
-    int page = key_page(c0);
-    stage_tile(c0, page);
+    const int page = key_page(c0);
     int page_next = key_page(c0 + 1);
 
     // ---- queries: thread = row tid / 2, half of its dims ----
@@ -238,6 +237,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = 0.0f;
         }
+        stage_tile(c0, page);                      // (the queries are on their way)
 #pragma unroll
         for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(x[i]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));

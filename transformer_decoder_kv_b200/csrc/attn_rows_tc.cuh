@@ -179,9 +179,8 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     }
 
     // ---- keys ----
-    // a tile is fetched by thread = key kr (4-bit cache: and half kh of its codes), and unpacked by
-    // warps 4..7 (K) and 0..3 (V), thread = key ku
-    const int kr = KV4 ? tid >> 1 : tid & 127, kh = tid & 1, ku = tid & 127;
+    // thread = key ku of a tile: fetched and K unpacked by warps 4..7, V unpacked by warps 0..3
+    const int ku = tid & 127;
     const bool k_side = warp >= 4;
     const int* tab = a.v.table ? a.v.table + s.slot * a.v.pages_per_slot : nullptr;
     const int pr_mask = a.v.shift == 31 ? 0x7fffffff : a.v.page_rows - 1;
@@ -191,37 +190,44 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     auto key_page = [&](int c) {
         int p = -1;
         if (c < c_end) {
-            const int j = unit_chunk(k, c) * kRtKeys + kr;
+            const int j = unit_chunk(k, c) * kRtKeys + ku;
             if (j < end) p = page_entry(j);
         }
         return p;
     };
     auto seen = [&](int j) { return j < end && (j >= seen_lo || j < a.sinks); };
-    // Copies the tile into its stage (4-bit cache), and notes its blocks without a page.
+    // Copies the tile into its stage (4-bit cache), and notes its blocks without a page: warps 4..7.
     auto stage_tile = [&](int c, int entry) {
+        if (!k_side) return;
         const int buf = (c - c0) & 1, pg = checked(entry);
         if (c < c_end) {
             if (KV4 && pg >= 0) {
-                const int pr = (unit_chunk(k, c) * kRtKeys + kr) & pr_mask;
+                const int pr = (unit_chunk(k, c) * kRtKeys + ku) & pr_mask;
                 const int part = a.v.page_rows * kKv4RowBytes;
-                const unsigned char* blk = a.cache + kv4_block(a.v, pg, hk);
-                unsigned char* dst = stages + buf * kRtStage;
-                cp_async16(dst + tid * 16, blk + pr * 32 + kh * 16);
-                cp_async16(dst + kRtV + tid * 16, blk + part + pr * 32 + kh * 16);
-                if ((kr & 3) == 0)                 // four keys' scales of K, of V
-                    cp_async16(dst + (kh ? kRtVs : kRtKs) + kr * 4, blk + kh * part + a.v.page_rows * 32 + pr * 4);
+                const unsigned char* src = a.cache + kv4_block(a.v, pg, hk) + pr * 32;
+                unsigned char* dst = stages + buf * kRtStage + ku * 32;
+                cp_async16(dst, src);
+                cp_async16(dst + 16, src + 16);
+                cp_async16(dst + kRtV, src + part);
+                cp_async16(dst + kRtV + 16, src + part + 16);
+                if ((ku & 3) == 0) {               // four keys' scales
+                    src += a.v.page_rows * 32 - pr * 28;
+                    dst = stages + buf * kRtStage + kRtKs + ku * 4;
+                    cp_async16(dst, src);
+                    cp_async16(dst + (kRtVs - kRtKs), src + part);
+                }
             }
-            if ((kr & 15) == 0) sm_bad[buf][kr >> 4] = pg < 0 && unit_chunk(k, c) * kRtKeys + kr < end;
+            if ((ku & 15) == 0) sm_bad[buf][ku >> 4] = pg < 0 && unit_chunk(k, c) * kRtKeys + ku < end;
         }
         if (KV4) cp_async_commit();
     };
 
     const int page = key_page(c0);
-    int page_next = key_page(c0 + 1);
+    int page1 = key_page(c0 + 1), page2 = key_page(c0 + 2);
 
     // ---- queries: thread = row tid / 2, half of its dims ----
     {
-        const int qr = tid >> 1;
+        const int qr = tid >> 1, kh = tid & 1;
         float x[32];
         float mx = 0.0f;
         if (qr < k.n_u) {
@@ -238,6 +244,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             for (int i = 0; i < 32; ++i) x[i] = 0.0f;
         }
         stage_tile(c0, page);                      // (the queries are on their way)
+        stage_tile(c0 + 1, page1);
 #pragma unroll
         for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(x[i]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -470,8 +477,6 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
 
     for (int c = c0; c < c_end; ++c) {
         const int j0 = unit_chunk(k, c) * kRtKeys;
-        stage_tile(c + 1, page_next);
-        const int page_after = key_page(c + 2);
         // this row's keys: 32-column masks, unless every row sees the whole tile
         const bool full = bad == 0 && j0 + kRtKeys - 1 <= p_first && j0 + kRtKeys <= end &&
                           (a.window == 0 || j0 > p_last - a.window || j0 + kRtKeys <= a.sinks);
@@ -490,20 +495,22 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
 
             // ---- softmax ----
             const float f = fmaxf(f_row * pow2i(ek - 10), 1.1754944e-38f);
-            float raw = -INFINITY;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 float x[32];
                 tmem_ld32(t_s + 32 * b, x);
-                if (full) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) raw = fmaxf(raw, x[i]);
-                } else {
+                if (!full) {
                     const uint32_t v = seen_bits(2 * half + b);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) raw = fmaxf(raw, (v >> i) & 1u ? x[i] : -INFINITY);
+                    for (int i = 0; i < 32; ++i) x[i] = (v >> i) & 1u ? x[i] : -INFINITY;
                 }
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) mx[n] = fmaxf(mx[n], fmaxf(x[i + 2 * n], x[i + 2 * n + 1]));
             }
+            float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             sm_x[half][row] = raw;
             pair_sync(1 + (warp & 3));
             raw = fmaxf(raw, sm_x[half ^ 1][row]);
@@ -611,7 +618,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         }
         const bool running = !plain, more = c + 1 < c_end;
         const float cf = corr * fac;               // (of this tile: preparing the next one may change fac)
-        plain = more && prepare(c + 1, page_next);
+        plain = more && prepare(c + 1, page1);
         if (running) {
             if (!mbar_wait_bounded(&bar_o, ph_o, nullptr)) s_fail = 1;
             ph_o ^= 1u;
@@ -629,8 +636,10 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             }
             tc_fence_before();
         }
-        if (more && !plain) store_v(c + 1, page_next);
-        page_next = page_after;
+        if (more && !plain) store_v(c + 1, page1);
+        stage_tile(c + 2, page2);                  // (the stage's last tile is unpacked)
+        page1 = page2;
+        page2 = key_page(c + 3);
     }
     // ---- finish ----
     __syncthreads();

@@ -49,7 +49,7 @@ static int check_units() {
         s.pos0 = static_cast<long long>((rnd() >> 8) % (cap + 40)) - 30;
         const int units = (s.n * a.group + UR - 1) / UR;
         for (int unit = 0; unit <= units; ++unit) {
-            const UnitKeys k = unit_keys<UR, CK>(a, s, unit, a.per_split);
+            const UnitKeys k = unit_keys<UR, CK>(a, s, unit);
             CHECK(unit < units ? k.n_u >= 1 && k.n_u <= UR : k.n_u == 0);
             if (!k.n_u) continue;
             CHECK(k.splits >= 1 && k.splits <= a.S && k.end <= cap && k.total >= 0);

@@ -32,7 +32,7 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_few(const Ro
     const StreamRows s = stream_rows(a.r, a.v, blockIdx.z);
     const int n_tiles = gridDim.y / a.v.heads;
     const int hk = blockIdx.y / n_tiles;
-    const UnitKeys k = unit_keys<R, kF32Chunk>(a, s, blockIdx.y % n_tiles, a.per_split);
+    const UnitKeys k = unit_keys<R, kF32Chunk>(a, s, blockIdx.y % n_tiles);
     const int sp = blockIdx.x;
     if (k.n_u == 0 || sp >= k.splits) return;
     const int c_end = split_begin(k, sp + 1);

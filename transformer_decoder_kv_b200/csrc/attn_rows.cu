@@ -20,7 +20,6 @@ struct RowsPlan {
     long long tiles, units;
     int most_splits;                                 // what the workspace is sized for
     int S, per_split;
-    bool on_device;                                  // the length of a split is chosen there
 };
 
 // Unit rows: the smallest few-row variant that holds a stream's rows of one group; the tensor-core
@@ -48,25 +47,18 @@ RowsPlan rows_shape(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, 
     const long long slots = static_cast<long long>(kRowsSms) * p.resident;
     const long long all = rows_max_chunks(view_dev(view), 1, 0, 0, p.chunk);
     p.most_splits = static_cast<int>(std::max(
-        1ll, std::min({static_cast<long long>(kRowsMaxSplits), (p.tc ? 6 : 2) * slots / p.units, all / p.least})));
+        1ll, std::min({static_cast<long long>(kRowsMaxSplits), (p.tc ? 8 : 2) * slots / p.units, all / p.least})));
     return p;
 }
 
-// Splits: the fewest (waves of resident blocks) x (rounds of chunks per block, and its start and end), a
-// merge counting as one more round. The blocks of the tensor-core tiles are few and long, so for them a
-// one-block kernel weighs the same from the batch's own lengths, within the splits launched here (a
-// block beyond a unit's splits ends at once, but takes its turn: at most six waves of them); a single
-// stream of many units, which gains nothing from that, is spared the extra launch.
+// Splits: the fewest (waves of resident blocks) x (rounds of chunks per block, and its start and end),
+// a merge counting as one more round. Of the tensor-core splits within a tenth of the best the finest
+// is taken, and its length is fixed, so that blocks of short and long streams are alike.
 void rows_splits(RowsPlan& p, const dec_kv_view& view, const dec_kv_rows& rows, int window, int sinks) {
     const long long span = std::min<long long>(rows.max_rows, p.unit_rows / p.group + 1);
     const int chunks = static_cast<int>(rows_max_chunks(view_dev(view), span, window, sinks, p.chunk));
     const int most = std::max(1, std::min(p.most_splits, chunks / p.least));
     const unsigned slots = kRowsSms * p.resident, start = p.tc ? 2 : 1;
-    p.on_device = p.tc && most > 1 && (rows.batch > 1 || 2 * p.units < slots);
-    if (p.on_device) {
-        p.S = std::min(most, 32);
-        return;
-    }
     auto cost = [&](unsigned S) {
         const unsigned rounds = ((chunks + S - 1) / S + p.warps - 1) / p.warps;
         return (static_cast<unsigned long long>(p.units) * S + slots - 1) / slots * (rounds + start) + (S > 1);
@@ -77,6 +69,9 @@ void rows_splits(RowsPlan& p, const dec_kv_view& view, const dec_kv_rows& rows, 
         const unsigned long long c = cost(S);
         if (c < best) best = c, p.S = S;
     }
+    if (p.tc)
+        for (int S = most; S > p.S; --S)
+            if (10 * cost(S) <= 11 * best) p.S = S;
     p.per_split = p.tc ? (chunks + p.S - 1) / p.S : p.least;
 }
 
@@ -109,7 +104,6 @@ template <bool KV4>
 cudaError_t launch_rows_tc(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
     thread_local int attr_dev = -1;
     cudaError_t e = prefer_max_shared_once(k_attn_rows_tc<KV4>, attr_dev, rt_smem_bytes<KV4>());
-    if (e == cudaSuccess && p.on_device) e = rows_launch(k_attn_split_length, dim3(1), kRtThreads, 0, st, a);
     if (e == cudaSuccess) e = launch_units(k_attn_rows_tc<KV4>, a, p, kRtThreads, rt_smem_bytes<KV4>(), st);
     return e == cudaSuccess ? launch_merge<kRtRows, kRtKeys>(a, p, st) : e;
 }
@@ -159,8 +153,7 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     a.sinks = sinks;
     a.out = out;
     a.out_ld = out_ld;
-    a.part = static_cast<float*>(workspace) + 64;      // 256 bytes behind the split length
-    a.split_length = plan.on_device ? static_cast<int*>(workspace) : nullptr;
+    a.part = static_cast<float*>(workspace);
     a.S = plan.S;
     a.per_split = plan.per_split;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);

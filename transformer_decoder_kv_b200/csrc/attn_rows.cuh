@@ -36,7 +36,6 @@ struct RowsAttnArgs {
     float* part;                 // [n_rows * heads, S] partial states
     int S;                       // splits launched per unit
     int per_split;               // chunks that make a split
-    int* split_length;           // that, where it is chosen on the device (else null)
 };
 
 // The keys of unit rows [u0, u0 + UR) of a stream in chunks of CK: chunks 0 .. sink_chunks - 1 and
@@ -49,7 +48,7 @@ struct UnitKeys {
 };
 
 template <int UR, int CK>
-__host__ __device__ __forceinline__ UnitKeys unit_keys(const RowsAttnArgs& a, const StreamRows& s, int unit, int per_split) {
+__host__ __device__ __forceinline__ UnitKeys unit_keys(const RowsAttnArgs& a, const StreamRows& s, int unit) {
     UnitKeys k{};
     const long long all = static_cast<long long>(s.n) * a.group;
     const long long u0 = static_cast<long long>(unit) * UR;
@@ -75,7 +74,7 @@ __host__ __device__ __forceinline__ UnitKeys unit_keys(const RowsAttnArgs& a, co
     k.sink_chunks = sc;
     k.first = fc;
     k.total = sc + static_cast<int>((k.end + CK - 1) / CK) - fc;
-    const int most = (k.total + per_split - 1) / per_split;
+    const int most = (k.total + a.per_split - 1) / a.per_split;
     k.splits = most < 1 ? 1 : (most < a.S ? most : a.S);
     return k;
 }
@@ -127,8 +126,7 @@ static __global__ void __launch_bounds__(128) k_attn_merge(const RowsAttnArgs a)
     const StreamRows s = stream_rows(a.r, a.v, blockIdx.z);
     const int i = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y;
     if (i >= s.n) return;
-    const UnitKeys k = unit_keys<UR, CK>(a, s, (i * a.group + h % a.group) / UR,
-                                         a.split_length ? __ldcg(a.split_length) : a.per_split);
+    const UnitKeys k = unit_keys<UR, CK>(a, s, (i * a.group + h % a.group) / UR);
     if (k.splits <= 1) return;
     const long long row = s.row0 + i;
     const float* p = a.part + (row * a.heads + h) * a.S * kPartStride;

@@ -137,57 +137,6 @@ __device__ __forceinline__ float4 rt_row4(const RowsAttnArgs& a, bool v, int pag
     return make_float4(val(0), val(1), val(2), val(3));
 }
 
-// Tiles per split, from the batch's own lengths, which the host does not know: of 1 .. S splits of the
-// longest unit, the count with the fewest (waves of resident blocks) x (tiles, and two for a block's
-// start and end). One block ahead of the attention kernel. (A stream's units are all taken as long as
-// its last one.)
-static __global__ void __launch_bounds__(kRtThreads) k_attn_split_length(const RowsAttnArgs a) {
-    __shared__ int sm_units[kRtThreads], sm_tiles[kRtThreads];
-    pdl_wait();
-    const int tid = threadIdx.x, lane = tid & 31;
-    long long blocks = 0;
-    int longest = 1;
-    for (int pass = 0; pass < 2; ++pass) {         // the longest unit, then the candidates' block counts
-        for (int b0 = 0; b0 < a.r.batch; b0 += kRtThreads) {
-            const int b = b0 + tid;
-            int units = 0, tiles = 0;
-            if (b < a.r.batch) {
-                const StreamRows s = stream_rows(a.r, a.v, b);
-                units = static_cast<int>((static_cast<long long>(s.n) * a.group + kRtRows - 1) / kRtRows);
-                if (units > 0) tiles = unit_keys<kRtRows, kRtKeys>(a, s, units - 1, 1).total;
-            }
-            __syncthreads();
-            sm_units[tid] = units;
-            sm_tiles[tid] = tiles;
-            __syncthreads();
-            if (tid < 32) {
-                const int n = min(kRtThreads, a.r.batch - b0);
-                if (pass == 0) {
-                    for (int i = lane; i < n; i += 32) longest = max(longest, sm_tiles[i]);
-                } else {
-                    const int len = (longest + lane) / (lane + 1);
-                    for (int i = 0; i < n; ++i) blocks += static_cast<long long>(sm_units[i]) * max(1, (sm_tiles[i] + len - 1) / len);
-                }
-            }
-        }
-        if (tid < 32 && pass == 0) longest = __reduce_max_sync(0xffffffffu, longest);
-    }
-    if (tid < 32) {
-        const int len = (longest + lane) / (lane + 1);
-        const long long waves = (blocks * a.v.heads + 2 * kRowsSms - 1) / (2 * kRowsSms);
-        // cost in the high bits, fewer splits first among equals
-        unsigned long long key = static_cast<unsigned long long>(waves * (len + 2)) * 32 + lane;
-        if (lane >= a.S) key = ~0ull;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
-            key = other < key ? other : key;
-        }
-        const int best = static_cast<int>(key & 31);
-        if (lane == 0) *a.split_length = (longest + best) / (best + 1);
-    }
-}
-
 template <bool KV4>
 static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const RowsAttnArgs a) {
     extern __shared__ unsigned char rt_raw[];
@@ -209,9 +158,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     const StreamRows s = stream_rows(a.r, a.v, blockIdx.z);
     const int n_tiles = gridDim.y / a.v.heads;
     const int hk = blockIdx.y / n_tiles;
-    const int unit = blockIdx.y - hk * n_tiles;
-    if (static_cast<long long>(unit) * kRtRows >= static_cast<long long>(s.n) * a.group) return;
-    const UnitKeys k = unit_keys<kRtRows, kRtKeys>(a, s, unit, a.split_length ? __ldcg(a.split_length) : a.per_split);
+    const UnitKeys k = unit_keys<kRtRows, kRtKeys>(a, s, blockIdx.y % n_tiles);
     const int sp = blockIdx.x;
     if (k.n_u == 0 || sp >= k.splits) return;
     const int c0 = split_begin(k, sp), c_end = split_begin(k, sp + 1);

@@ -22,14 +22,17 @@ struct RowsPlan {
     int S, per_split;
 };
 
-// Unit rows: the smallest few-row variant that holds a stream's rows of one group; the tensor-core
-// tiles of 128 rows from where the widest few-row variant would need several units. The bound on the
-// splits does not depend on the window.
+// Unit rows: the smallest few-row variant that holds a stream's rows of one group, several units of the
+// widest one, and the tensor-core tiles of 128 rows where those take longer. Measured on B200, few-row
+// units against tiles, us: 4-bit cache, 32 streams x 1024 rows x 16 heads, 32 rows 56 / 86, 48 rows
+// 83 / 87, and 32 x 2048 x 2 heads, 63 rows 26 / 29 (a further unit adds 27; the tile does not change);
+// f32 cache, the same streams, 16 rows 179 / 208, 20 rows 254 / 208. The bound on the splits does not
+// depend on the window.
 RowsPlan rows_shape(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, int n_heads) {
     RowsPlan p{};
     p.group = n_heads / view.n_kv_heads;
     const long long u = static_cast<long long>(rows.max_rows) * p.group;
-    p.tc = u > (kv4 ? 32 : 8);
+    p.tc = u > (kv4 ? 64 : 16);
     if (p.tc) {
         p.unit_rows = kRtRows;
         p.resident = 2, p.warps = 1, p.chunk = kRtKeys, p.least = 1;
@@ -53,7 +56,8 @@ RowsPlan rows_shape(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, 
 
 // Splits: the fewest (waves of resident blocks) x (rounds of chunks per block, and its start and end),
 // a merge counting as one more round. Of the tensor-core splits within a tenth of the best the finest
-// is taken, and its length is fixed, so that blocks of short and long streams are alike.
+// is taken; where they make more than one wave their length is fixed, so that the blocks of short and
+// long streams are alike (in one wave a short stream is rather split as often as it can be).
 void rows_splits(RowsPlan& p, const dec_kv_view& view, const dec_kv_rows& rows, int window, int sinks) {
     const long long span = std::min<long long>(rows.max_rows, p.unit_rows / p.group + 1);
     const int chunks = static_cast<int>(rows_max_chunks(view_dev(view), span, window, sinks, p.chunk));
@@ -72,7 +76,7 @@ void rows_splits(RowsPlan& p, const dec_kv_view& view, const dec_kv_rows& rows, 
     if (p.tc)
         for (int S = most; S > p.S; --S)
             if (10 * cost(S) <= 11 * best) p.S = S;
-    p.per_split = p.tc ? (chunks + p.S - 1) / p.S : p.least;
+    p.per_split = !p.tc ? p.least : p.units * p.S <= slots ? 2 : (chunks + p.S - 1) / p.S;
 }
 
 size_t rows_workspace(const RowsPlan& p, const dec_kv_rows& rows, int n_heads) {

@@ -150,7 +150,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     __shared__ uint32_t s_tmem;
     __shared__ float sm_f[kRtRows], sm_x[2][kRtRows];            // row factors; column halves' maxima, sums
     __shared__ uint32_t sm_bad[2][8];                            // of a tile's 16-key blocks: no page
-    __shared__ uint32_t sm_mag[8];                               // f32: magnitudes
+    __shared__ uint32_t sm_mag[2][8];                            // f32: magnitudes of K, of V
     __shared__ int s_fail;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -179,8 +179,9 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     }
 
     // ---- keys ----
-    // thread = key ku of a tile: fetched and K unpacked by warps 4..7, V unpacked by warps 0..3
-    const int ku = tid & 127;
+    // a 4-bit tile: thread = key ku, fetched and K unpacked by warps 4..7, V unpacked by warps 0..3; an f32
+    // tile: thread = half kh of key ku's dims
+    const int ku = KV4 ? tid & 127 : tid >> 1, kh = tid & 1;
     const bool k_side = warp >= 4;
     const int* tab = a.v.table ? a.v.table + s.slot * a.v.pages_per_slot : nullptr;
     const int pr_mask = a.v.shift == 31 ? 0x7fffffff : a.v.page_rows - 1;
@@ -196,9 +197,9 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         return p;
     };
     auto seen = [&](int j) { return j < end && (j >= seen_lo || j < a.sinks); };
-    // Copies the tile into its stage (4-bit cache), and notes its blocks without a page: warps 4..7.
+    // Copies the tile into its stage (4-bit cache), and notes its blocks without a page.
     auto stage_tile = [&](int c, int entry) {
-        if (!k_side) return;
+        if (KV4 && !k_side) return;
         const int buf = (c - c0) & 1, pg = checked(entry);
         if (c < c_end) {
             if (KV4 && pg >= 0) {
@@ -227,7 +228,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
 
     // ---- queries: thread = row tid / 2, half of its dims ----
     {
-        const int qr = tid >> 1, kh = tid & 1;
+        const int qr = tid >> 1;
         float x[32];
         float mx = 0.0f;
         if (qr < k.n_u) {
@@ -348,12 +349,12 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             }
         }
     };
-    // f32: half hf of key ku's dims, 0 where no row sees the key.
-    auto load_f32 = [&](int c, int entry, const float* pool, int hf, float4 (&x)[8]) {
+    // f32: this thread's 32 dims of K or V, 0 where no row sees the key.
+    auto load_f32 = [&](int c, int entry, const float* pool, float4 (&x)[8]) {
         const int j = unit_chunk(k, c) * kRtKeys + ku, pg = checked(entry);
         const bool live = pg >= 0 && seen(j);
         const float4* src = reinterpret_cast<const float4*>(
-            pool + (live ? kvf_block(a.v, pg, hk) + static_cast<long long>(j & pr_mask) * kHeadDim + hf * 32 : 0));
+            pool + (live ? kvf_block(a.v, pg, hk) + static_cast<long long>(j & pr_mask) * kHeadDim + kh * 32 : 0));
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = live ? __ldg(src + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     };
@@ -366,27 +367,20 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
                     max(__float_as_uint(fabsf(x[n].z)), __float_as_uint(fabsf(x[n].w))));
         return g;
     };
-    // f32: key ku's K or V scaled, split and stored; returns the largest magnitude.
-    auto copy_f32 = [&](int c, int entry, const float* pool, unsigned char* plane, float up) {
-        uint32_t g = 0;
+    // f32: scales, splits and stores.
+    auto store_f32 = [&](unsigned char* plane, const float4 (&x)[8], float up) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            float4 x[8];
-            load_f32(c, entry, pool, hf, x);
-            g = max(g, magnitude(x));
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float4 u = x[2 * w], v = x[2 * w + 1];
-                const float y[8] = {u.x * up, u.y * up, u.z * up, u.w * up, v.x * up, v.y * up, v.z * up, v.w * up};
-                rt_store_split<false>(plane, plane + kRtPlane, ku, hf * 4 + w, y);
-            }
+        for (int w = 0; w < 4; ++w) {
+            const float4 u = x[2 * w], v = x[2 * w + 1];
+            const float y[8] = {u.x * up, u.y * up, u.z * up, u.w * up, v.x * up, v.y * up, v.z * up, v.w * up};
+            rt_store_split<false>(plane, plane + kRtPlane, ku, kh * 4 + w, y);
         }
-        return g;
     };
+    float4 vf[KV4 ? 1 : 8];                        // f32: the next tile's V
 
-    // Gets tile c ready for its scores: looks it over, and K into sK by warps 4..7 (every thread is done
-    // with the last tile's scores). True when something that a row sees is not finite: the tile is left
-    // to the plain loop. All threads return the same.
+    // Gets tile c ready for its scores: looks it over, and K into sK (every thread is done with the last
+    // tile's scores), an f32 V into registers. True when something that a row sees is not finite: the
+    // tile is left to the plain loop. All threads return the same.
     auto prepare = [&](int c, int entry) -> bool {
         fac = 1.0f;
         bool plain = false;
@@ -398,32 +392,31 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         } else {
             // The powers of two stand while the values stay within 2^6 of the largest one met when they
             // were set; a tile beyond them (the first one, to begin with) sets them anew.
-            uint32_t mag;
-            if (k_side) {
-                mag = copy_f32(c, entry, a.k, sK, pow2i(10 - ek));
-            } else {
-                float4 x[8], y[8];
-                load_f32(c, entry, a.vv, 0, x);
-                load_f32(c, entry, a.vv, 1, y);
-                mag = max(magnitude(x), magnitude(y));
-            }
-            const uint32_t lim = static_cast<uint32_t>(min(127 + (k_side ? ek : E) + 6, 255)) << 23;
+            float4 x[8];
+            load_f32(c, entry, a.k, x);
+            uint32_t km = magnitude(x);
+            store_f32(sK, x, pow2i(10 - ek));
+            load_f32(c, entry, a.vv, vf);
+            uint32_t vm = magnitude(vf);
+            const uint32_t klim = static_cast<uint32_t>(min(127 + ek + 6, 255)) << 23;
+            const uint32_t vlim = static_cast<uint32_t>(min(127 + E + 6, 255)) << 23;
             fence_async_smem();
-            if (__syncthreads_or(c == c0 || mag >= lim)) {
-                mag = __reduce_max_sync(0xffffffffu, mag);
-                if (lane == 0) sm_mag[warp] = mag;
+            if (__syncthreads_or(c == c0 || km >= klim || vm >= vlim)) {
+                km = __reduce_max_sync(0xffffffffu, km);
+                vm = __reduce_max_sync(0xffffffffu, vm);
+                if (lane == 0) sm_mag[0][warp] = km, sm_mag[1][warp] = vm;
                 __syncthreads();
-                uint32_t km = 0, vm = 0;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    vm = max(vm, sm_mag[w]);
-                    km = max(km, sm_mag[4 + w]);
+                for (int w = 0; w < 8; ++w) {
+                    km = max(km, sm_mag[0][w]);
+                    vm = max(vm, sm_mag[1][w]);
                 }
                 plain = max(km, vm) >= 0x7f800000u;
                 if (!plain) {
                     ek = max(ek, static_cast<int>(km >> 23) - 127);
                     raise_E(static_cast<int>(vm >> 23) - 127);
-                    if (k_side) copy_f32(c, entry, a.k, sK, pow2i(10 - ek));
+                    load_f32(c, entry, a.k, x);
+                    store_f32(sK, x, pow2i(10 - ek));
                 }
                 fence_async_smem();
                 __syncthreads();
@@ -461,17 +454,20 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         for (int i = 0; i < 4; ++i) umma_f16_ss(tmem, qh + 2 * i, kd + 2 * i, id, 1);
         umma_commit(&bar_s);
     };
-    // V of tile c into sV by warps 0..3; every thread has seen the last P V end.
-    auto store_v = [&](int c, int entry) {
-        if (k_side) return;
-        if constexpr (KV4) unpack_v4(c); else copy_f32(c, entry, a.vv, sV, pow2i(10 - E));
+    // V of tile c into sV; every thread has seen the last P V end.
+    auto store_v = [&](int c) {
+        if constexpr (KV4) {
+            if (!k_side) unpack_v4(c);
+        } else {
+            store_f32(sV, vf, pow2i(10 - E));
+        }
     };
     bool plain = false;
     if (c0 < c_end) {
         plain = prepare(c0, page);
         if (!plain) {
             start_scores();
-            store_v(c0, page);
+            store_v(c0);
         }
     }
 
@@ -626,17 +622,21 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         }
         if (more && !plain) start_scores();        // (over the columns that P V has read)
         if (running) {
-            float d[32];
-            tmem_ld32(t_o, d);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const float2 y = fma2(make_float2(o[i], o[i + 1]), make_float2(cf, cf), make_float2(d[i], d[i + 1]));
-                o[i] = y.x;
-                o[i + 1] = y.y;
+            for (int b = 0; b < 2; ++b) {
+                float d[16];
+                tmem_ld16(t_o + 16 * b, d);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    float* x = o + 16 * b + i;
+                    const float2 y = fma2(make_float2(x[0], x[1]), make_float2(cf, cf), make_float2(d[i], d[i + 1]));
+                    x[0] = y.x;
+                    x[1] = y.y;
+                }
             }
             tc_fence_before();
         }
-        if (more && !plain) store_v(c + 1, page1);
+        if (more && !plain) store_v(c + 1);
         stage_tile(c + 2, page2);                  // (the stage's last tile is unpacked)
         page1 = page2;
         page2 = key_page(c + 3);

@@ -508,7 +508,8 @@ dec_status dec_i8_dot(const int8_t* xq, const int8_t* wq, int32_t m, int32_t n, 
  *              stored and read back as zeros; a query below position 0 gives zeros.
  * The structs are host memory, read during the call; the device arrays are read by the queued
  * kernels. The calls need no handle, allocate nothing, run on the calling thread's current
- * device, do not synchronise, and can be captured into CUDA graphs. Errors set
+ * device, do not synchronise, and can be captured into CUDA graphs (make a first call on the
+ * device before: it may load the module); a replay reads the device arrays anew. Errors set
  * dec_last_error(NULL).
  */
 typedef struct dec_kv_view {
@@ -562,8 +563,12 @@ dec_status dec_kv4_read(const dec_kv_view* view, const dec_kv_rows* rows, const 
  * (window 0: no limit) or j < sinks (the first tokens, which stay visible). For each head h, with
  * the K/V head h / (n_heads / n_kv_heads): s_j = q . k_j / 8, max-subtracted softmax in f32,
  * out = sum_j p_j v_j. A row that sees no key, or whose softmax sum is not finite and positive,
- * gives zeros, as in dec_attention. Values of keys a query does not see never reach it, whatever
- * they are (NaN, infinities, rows never written).
+ * gives zeros, as in dec_attention (a query with an element of 2^112 or more may be taken as one,
+ * and a bounded device wait that gives up, after about a second, leaves its rows zero). Values of
+ * keys a query does not see never reach it, whatever they are (NaN, infinities, rows never
+ * written). A row's result depends on its own stream and on the batch's shape (batch, max_rows,
+ * n_heads, the view), which decides how its keys are split, not on the other streams' contents or
+ * on when blocks run: equal calls give equal bits.
  *   q, out    device f32 [n_rows] rows of n_heads * 64, q_ld and out_ld floats apart (multiples of 4)
  *   n_heads   a multiple of n_kv_heads
  *   workspace device scratch of dec_attention_rows_workspace_size(view, rows, n_heads) bytes. Its

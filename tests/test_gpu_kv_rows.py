@@ -320,3 +320,115 @@ def test_window_zero_sinks_zero_equals_dec_attention_within_rounding():
     torch.cuda.synchronize()
     _, tol = s.reference(False, 0, 0)
     check(out.cpu().numpy().reshape(B, H, D), want.cpu().numpy().astype(np.float64), 2 * tol)
+
+
+@pytest.mark.parametrize("rows", [1, 40, 130])
+@pytest.mark.parametrize("kv4", [True, False], ids=["kv4", "f32"])
+def test_pools_beyond_32_bit_offsets(kv4, rows):
+    """The same pages at the bottom of a small pool and at the top of one whose offsets pass 32 bits."""
+    import torch
+    import transformer_decoder_kv_b200 as pkg
+    HK, H, pr, n_len = 8, 16, 64, 300
+    far = 125_000 if kv4 else 70_000             # 36,864 bytes (kv4), 32,768 floats (f32) a page
+    assert far * (36_864 if kv4 else 32_768) > 1 << (32 if kv4 else 31)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((n_len, HK * D), device="cuda", generator=g) for _ in range(2))
+    q = torch.randn((rows, H * D), device="cuda", generator=g)
+    outs = []
+    for n_pages in (5, far):
+        table = i32([[n_pages - 1 - i for i in range(5)]])
+        view = pkg.KvView(HK, pr, 5, 1, n_pages, table)
+        batch = pkg.KvRows(1, i32([n_len]), None, i32([0, rows]), rows, rows)
+        every = pkg.KvRows(1, i32([n_len]), None, i32([0, n_len]), n_len, n_len)
+        nb = pkg.attention_rows_workspace_size(view, batch, H)
+        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(q)
+        if kv4:
+            cache = torch.empty(pkg.kv4_bytes(view), dtype=torch.uint8, device="cuda")
+            pkg.kv4_write(view, every, k, v, cache)
+            ko, vo = torch.empty_like(k), torch.empty_like(v)
+            pkg.kv4_read(view, every, cache, ko, vo)
+            assert np.array_equal(ko.cpu().numpy().reshape(-1, D), kv4_values(k.cpu().numpy().reshape(-1, D)))
+            pkg.attention_kv4(view, batch, q, cache, H, out, ws, nb, 100, 3)
+        else:
+            pools = []
+            for x in (k, v):
+                pool = torch.empty((n_pages, HK, pr, D), device="cuda")
+                for lp in range(5):
+                    part = x[lp * pr:(lp + 1) * pr].view(-1, HK, D)
+                    pool[n_pages - 1 - lp, :, :len(part)] = part.transpose(0, 1)
+                pools.append(pool)
+            pkg.attention_window(view, batch, q, *pools, H, out, ws, nb, 100, 3)
+        outs.append(out)
+    assert torch.equal(*outs) and torch.isfinite(outs[0]).all()
+
+
+@pytest.mark.parametrize("shape", ["gqa7", "ragged_gqa"])
+@pytest.mark.parametrize("kv4", [True, False], ids=["kv4", "f32"])
+def test_calls_that_overlap_on_two_streams(kv4, shape):
+    s = setup(shape)
+    t = s.torch
+    caches = s.new_cache() if kv4 else s.f32_pools()
+    if kv4:
+        s.write_all(caches)
+    s.qd = s.f32(s.q.reshape(s.n_buf, -1))
+    want = [s.attend(kv4, w, 2, caches) for w in (0, 70)]
+    streams = [t.cuda.Stream() for _ in range(2)]
+    nb = s.pkg.attention_rows_workspace_size(s.view, s.batch, s.H)
+    ws = [t.empty(nb, dtype=t.uint8, device="cuda") for _ in range(2)]
+    outs = [t.full_like(want[0], 7.5) for _ in range(2)]
+    t.cuda.synchronize()
+    for _ in range(20):
+        for i, w in enumerate((0, 70)):
+            s.attend(kv4, w, 2, caches, out=outs[i], ws=ws[i], stream=streams[i].cuda_stream)
+    t.cuda.synchronize()
+    assert t.equal(outs[0], want[0]) and t.equal(outs[1], want[1])
+
+
+@pytest.mark.parametrize("kv4", [True, False], ids=["kv4", "f32"])
+def test_shared_slots_shared_pages_and_a_row_limit(kv4):
+    """One slot in two streams, two slots with the same first pages, and a stream with more rows than
+    max_rows: its first ones are processed, the others left."""
+    import torch
+    s = Setup(4, 2, [100, 100], [2, 2], 16, True, seed=1, pad_rows=0)
+    caches = s.new_cache() if kv4 else s.f32_pools()
+    if kv4:
+        s.write_all(caches)
+    s.q[2:4] = s.q[:2]
+    table = s.table.copy()
+    table[s.slots[1], :] = table[s.slots[0], :]
+    for view, slots in ((s.view, [s.slots[0]] * 2), (s.pkg.KvView(2, 16, s.pps, s.n_slots, s.n_pages, s.i32(table)), s.slots)):
+        s.view = view
+        s.batch = s.pkg.KvRows(2, s.i32([100, 100]), s.i32(slots), s.i32([0, 2, 4]), 4, 2)
+        out = s.attend(kv4, 0, 0, caches)
+        assert torch.equal(out[:2], out[2:]) and torch.isfinite(out).all()
+    s.batch = s.pkg.KvRows(2, s.i32([100, 100]), s.i32(slots), s.i32([0, 2, 4]), 4, 1)
+    out = s.attend(kv4, 0, 0, caches)
+    assert (out[1] == 7.5).all() and (out[3] == 7.5).all()
+    ref, tol = attention(s.q[:1], *(kv4_values(x[0]) if kv4 else x[0] for x in (s.k, s.v)), [98], 0, 0)
+    check(out[:1].cpu().numpy().reshape(ref.shape), ref, tol)
+
+
+def test_largest_batch():
+    import torch
+    import transformer_decoder_kv_b200 as pkg
+    B = 65535
+    view = pkg.KvView(1, 16, 1, 1)
+    lens = torch.arange(B, dtype=torch.int32, device="cuda") % 17
+    slots = torch.zeros(B, dtype=torch.int32, device="cuda")
+    cache = torch.empty(pkg.kv4_bytes(view), dtype=torch.uint8, device="cuda")
+    kv = torch.randn((16, D), device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    pkg.kv4_write(view, pkg.KvRows(1, i32([16]), None, i32([0, 16]), 16, 16), kv, kv, cache)
+    batch = pkg.KvRows(B, lens, slots)
+    q = torch.randn((1, D), device="cuda").expand(B, D).contiguous()
+    out = torch.full((B, D), 7.5, device="cuda")
+    nb = pkg.attention_rows_workspace_size(view, batch, 1)
+    pkg.attention_kv4(view, batch, q, cache, 1, out, torch.empty(nb, dtype=torch.uint8, device="cuda"), nb)
+    assert (out[lens == 0] == 0).all()
+    for n in (1, 16):
+        rows = out[lens == n]
+        assert (rows == rows[0]).all()
+    values = kv4_values(kv.cpu().numpy())
+    assert np.allclose(out[1].cpu().numpy(), values[0], rtol=1e-5)

@@ -124,6 +124,15 @@ def test_binding_checks_types_shapes_and_devices():
         b._row_buffer("q", torch.zeros((2, 64), dtype=torch.float16), 2, 64)
     with pytest.raises(b.DecError, match="CUDA"):
         b._row_buffer("q", torch.zeros((2, 64)), 2, 64)
+    with pytest.raises(b.DecError, match="device tensor"):
+        b.KvRows(2, [1, 2])
+    with pytest.raises(b.DecError, match="device tensor"):
+        b._row_buffer("q", [[0.0] * 64], 1, 64)
+    rows = type("Rows", (), {"device": None})()
+    for ws, n, word in ((torch.zeros(4), 17, "needs 17"), (torch.zeros(8)[::2], 16, "contiguous"),
+                        (torch.zeros(4), 16, "CUDA"), (object(), 16, "device tensor")):
+        with pytest.raises(b.DecError, match=word):
+            b._scratch(rows, ws, n)
     with pytest.raises(b.DecError, match="bad view"):
         b.kv4_bytes(b.KvView(1, 48, 2, 1))
 

@@ -395,14 +395,25 @@ def _device_array(name: str, a, dtype: str, least: int, device=None) -> Optional
         if a.device != device if device is not None else not a.is_cuda:
             _einval(f"{name}: must be on {device or 'a CUDA device'}, is on {a.device}")
         return a.data_ptr()
-    return _ptr(a)
+    _einval(f"{name}: must be a device tensor")
+
+
+def _scratch(rows, workspace, workspace_bytes: int) -> Optional[int]:
+    """Pointer of a workspace of at least workspace_bytes on the batch's device."""
+    if not hasattr(workspace, "data_ptr"):
+        _einval("workspace: must be a device tensor")
+    if workspace.nbytes < workspace_bytes or not workspace.is_contiguous():
+        _einval(f"workspace: {workspace.nbytes} bytes (contiguous: {workspace.is_contiguous()}), needs {workspace_bytes}")
+    if workspace.device != rows.device if rows.device is not None else not workspace.is_cuda:
+        _einval(f"workspace: must be on {rows.device or 'a CUDA device'}, is on {workspace.device}")
+    return workspace.data_ptr()
 
 
 def _row_buffer(name: str, a, n_rows: int, width: int, device=None):
     """(pointer, floats between rows) of f32 rows: [n_rows, width] or [n_rows, heads, 64] with
     contiguous rows, any row stride."""
     if not hasattr(a, "data_ptr"):
-        return _ptr(a), width
+        _einval(f"{name}: must be a device tensor")
     if str(a.dtype) != "torch.float32":
         _einval(f"{name}: expected float32, got {a.dtype}")
     if not a.is_cuda or (device is not None and a.device != device):
@@ -522,7 +533,8 @@ def attention_kv4(view: KvView, rows: KvRows, q, cache, n_heads: int, out, works
     qp, q_ld = _rows_2d("q", q, rows, n_heads * 64)
     op, o_ld = _rows_2d("out", out, rows, n_heads * 64)
     _raise_thread_error(lib().dec_attention_kv4(view.ref, rows.ref, qp, q_ld, n_heads, _pool(view, rows, cache), window, sinks,
-                                                op, o_ld, _ptr(workspace), workspace_bytes, stream))
+                                                op, o_ld, _scratch(rows, workspace, workspace_bytes), workspace_bytes,
+                                                stream))
 
 
 def attention_window(view: KvView, rows: KvRows, q, k, v, n_heads: int, out, workspace, workspace_bytes: int,
@@ -535,4 +547,5 @@ def attention_window(view: KvView, rows: KvRows, q, k, v, n_heads: int, out, wor
     kp = _device_array("k", k, "float32", least, rows.device)
     vp = _device_array("v", v, "float32", least, rows.device)
     _raise_thread_error(lib().dec_attention_window(view.ref, rows.ref, qp, q_ld, n_heads, kp, vp, window, sinks, op,
-                                                   o_ld, _ptr(workspace), workspace_bytes, stream))
+                                                   o_ld, _scratch(rows, workspace, workspace_bytes), workspace_bytes,
+                                                   stream))

@@ -38,7 +38,7 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_few(const Ro
     const int c_end = split_begin(k, sp + 1);
     const int end = static_cast<int>(k.end);
 
-    // queries, times log2(e) / 8: scores are in the log2 domain
+    // (scores are taken to the log2 domain)
     float4 q[R];
     float o[R][4], m[R], l[R];
 #pragma unroll

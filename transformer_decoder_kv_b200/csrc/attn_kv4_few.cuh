@@ -150,6 +150,28 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
         return p;
     };
     int pg = quarter_page(c0);
+
+    // the queries of column g of each tile, dims 8 t .. 8 t + 7 of both groups, fetched meanwhile
+    float qx[NT][2][8];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int u = PAIR ? g >> 1 : nt * 8 + g;
+        if (u < k.n_u) {
+            const int ur = k.u0 + u, i = ur / a.group, h = hk * a.group + ur % a.group;
+            const float4* q = reinterpret_cast<const float4*>(a.q + static_cast<long long>(s.row0 + i) * a.q_ld +
+                                                              h * kHeadDim + 8 * t);
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr) {
+                const float4 x0 = q[gr * 8], x1 = q[gr * 8 + 1];
+                float* x = qx[nt][gr];
+                x[0] = x0.x, x[1] = x0.y, x[2] = x0.z, x[3] = x0.w;
+                x[4] = x1.x, x[5] = x1.y, x[6] = x1.z, x[7] = x1.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) qx[nt][0][j] = qx[nt][1][j] = 0.0f;
+        }
+    }
     uint32_t bad[2] = {0, 0};              // per stage: lanes whose quarter has no page
     auto issue = [&](int c, int stage) {
         if (c < c_end) {
@@ -174,29 +196,14 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
     };
     issue(c0, 0);
 
-    // ---- Q^T fragments: column g of each tile, dims 8 t .. 8 t + 7 of both groups ----
+    // ---- Q^T fragments ----
     uint32_t qf[NB][NT][4][2];             // PAIR: one part per column; else high, low
     // score factors of this thread's rows; -8 sum(q) of columns 2 t, 2 t + 1: where the accumulators
     // start, and (not PAIR) the remainders' part
     float qs[NT][NB], off[NT][2][2], rem[NT][2][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int u = PAIR ? g >> 1 : nt * 8 + g;
-        float x[2][8];
-        if (u < k.n_u) {
-            const int ur = k.u0 + u, i = ur / a.group, h = hk * a.group + ur % a.group;
-            const float4* q = reinterpret_cast<const float4*>(a.q + static_cast<long long>(s.row0 + i) * a.q_ld +
-                                                              h * kHeadDim + 8 * t);
-#pragma unroll
-            for (int gr = 0; gr < 2; ++gr) {
-                const float4 x0 = q[gr * 8], x1 = q[gr * 8 + 1];
-                x[gr][0] = x0.x, x[gr][1] = x0.y, x[gr][2] = x0.z, x[gr][3] = x0.w;
-                x[gr][4] = x1.x, x[gr][5] = x1.y, x[gr][6] = x1.z, x[gr][7] = x1.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[0][j] = x[1][j] = 0.0f;
-        }
+        const float (&x)[2][8] = qx[nt];
         float mx = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(fabsf(x[0][j]), fabsf(x[1][j])));
@@ -379,14 +386,20 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
                 }
                 // (the raw sums are below 1: no scale takes them out of f32's range)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const float f = qs[nt][b];
-                        const float r0 = PAIR ? d0[2 * j] + d0[2 * j + 1] : d0[2 * j + b] + rem[nt][0][b];
-                        const float r1 = PAIR ? d1[2 * j] + d1[2 * j + 1] : d1[2 * j + b] + rem[nt][1][b];
-                        sc[nt][b][mt][j] = fmaf(r1, ks1[j], r0 * ks0[j]) * f;
+                for (int j = 0; j < 2; ++j) {
+                    if (PAIR) {
+                        const float r0 = d0[2 * j] + d0[2 * j + 1], r1 = d1[2 * j] + d1[2 * j + 1];
+                        sc[nt][0][mt][j] = fmaf(r1, ks1[j], r0 * ks0[j]) * qs[nt][0];
+                    } else {
+                        // both rows of the thread at once
+                        const float2 r0 = add2(make_float2(d0[2 * j], d0[2 * j + 1]), make_float2(rem[nt][0][0], rem[nt][0][1]));
+                        const float2 r1 = add2(make_float2(d1[2 * j], d1[2 * j + 1]), make_float2(rem[nt][1][0], rem[nt][1][1]));
+                        const float2 x = fma2(r1, make_float2(ks1[j], ks1[j]), mul2(r0, make_float2(ks0[j], ks0[j])));
+                        const float2 y = mul2(x, make_float2(qs[nt][0], qs[nt][NB - 1]));
+                        sc[nt][0][mt][j] = y.x;
+                        sc[nt][NB - 1][mt][j] = y.y;
                     }
+                }
             }
         }
         if (!full) {
@@ -488,8 +501,13 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    o[nt][mt][j] = fmaf(o[nt][mt][j], corr[nt][PAIR ? 0 : j & 1], d[nt][mt][j]);
+                for (int j = 0; j < 4; j += 2) {
+                    const float2 y = fma2(make_float2(o[nt][mt][j], o[nt][mt][j + 1]),
+                                          make_float2(corr[nt][0], corr[nt][NB - 1]),
+                                          make_float2(d[nt][mt][j], d[nt][mt][j + 1]));
+                    o[nt][mt][j] = y.x;
+                    o[nt][mt][j + 1] = y.y;
+                }
         if (any_nan) {                     // a seen key whose V group is not a number
 #pragma unroll
             for (int w = 0; w < 2; ++w) {

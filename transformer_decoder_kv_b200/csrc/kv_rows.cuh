@@ -87,13 +87,21 @@ __host__ __device__ __forceinline__ long long kvf_block(const KvViewDev& v, int 
     return (static_cast<long long>(page) * v.heads + head) * v.page_rows * kHeadDim;
 }
 
-// Packed f32 pairs: a * b + c and a + b on both halves.
+// Packed f32 pairs: a * b + c, a * b and a + b on both halves.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
     asm("{.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
         "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {

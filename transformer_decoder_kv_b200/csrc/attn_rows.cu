@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "attn_f32_few.cuh"
+#include "attn_f32_mma.cuh"
 #include "attn_kv4_few.cuh"
 #include "attn_rows.cuh"
 #include "attn_rows_tc.cuh"
@@ -23,16 +24,18 @@ struct RowsPlan {
 };
 
 // Unit rows: the smallest few-row variant that holds a stream's rows of one group, several units of the
-// widest one, and the tensor-core tiles of 128 rows where those take longer. Measured on B200, few-row
-// units against tiles, us: 4-bit cache, 32 streams x 1024 rows x 16 heads, 32 rows 56 / 86, 48 rows
-// 83 / 87, and 32 x 2048 x 2 heads, 63 rows 26 / 29 (a further unit adds 27; the tile does not change);
-// f32 cache, the same streams, 16 rows 179 / 208, 20 rows 254 / 208. The bound on the splits does not
-// depend on the window.
+// widest one, and the tensor-core tiles of 128 rows where those take longer. Measured on B200, us.
+//   4-bit cache, units against tiles (a further unit of 16 rows adds 27, the tile does not change):
+//     32 streams x 1024 rows x 16 heads, 32 rows 56 / 86, 48 rows 83 / 87; 32 x 2048 x 2, 63 rows 26 / 29
+//   f32 cache, the same streams: 32 rows (two units of 16) 137 / 208, a third unit would add 60
+//   f32 cache, CUDA cores against mma.sync: 256 streams x 4096 x 4 heads, 3 rows 364 / 390; 256 x 8192 x 1,
+//     4 rows 226 / 204; 256 x 8192 x 2, 7 rows 689 / 401, 16 rows 1306 / 491
+// The bound on the splits does not depend on the window.
 RowsPlan rows_shape(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, int n_heads) {
     RowsPlan p{};
     p.group = n_heads / view.n_kv_heads;
     const long long u = static_cast<long long>(rows.max_rows) * p.group;
-    p.tc = u > (kv4 ? 64 : 16);
+    p.tc = u > (kv4 ? 64 : 32);
     if (p.tc) {
         p.unit_rows = kRtRows;
         p.resident = 2, p.warps = 1, p.chunk = kRtKeys, p.least = 1;
@@ -41,8 +44,8 @@ RowsPlan rows_shape(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, 
         p.resident = u <= 4 ? 4 : u <= 8 ? 3 : 2;
         p.warps = kFewWarps, p.chunk = kFewChunk, p.least = kFewWarps;
     } else {
-        p.unit_rows = u <= 1 ? 1 : u <= 2 ? 2 : u <= 4 ? 4 : 8;
-        p.resident = u <= 4 ? 4 : 3;
+        p.unit_rows = u <= 1 ? 1 : u <= 2 ? 2 : u <= 8 ? 8 : 16;
+        p.resident = u <= 2 ? 4 : 2;
         p.warps = kF32Warps, p.chunk = kF32Chunk, p.least = 2 * kF32Warps;
     }
     p.tiles = (u + p.unit_rows - 1) / p.unit_rows;
@@ -118,6 +121,12 @@ cudaError_t launch_f32_few(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_
     return e == cudaSuccess ? launch_merge<R, kF32Chunk>(a, p, st) : e;
 }
 
+template <int NT>
+cudaError_t launch_f32_mma(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
+    const cudaError_t e = launch_units(k_attn_f32_mma<NT>, a, p, kF32Warps * 32, 0, st);
+    return e == cudaSuccess ? launch_merge<8 * NT, kF32Chunk>(a, p, st) : e;
+}
+
 template <bool KV4>
 dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows* rows, const float* q, int64_t q_ld,
                      int32_t n_heads, const void* cache, const float* k, const float* v, int32_t window,
@@ -171,8 +180,8 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     else
         e = plan.unit_rows == 1   ? launch_f32_few<1>(a, plan, st)
             : plan.unit_rows == 2 ? launch_f32_few<2>(a, plan, st)
-            : plan.unit_rows == 4 ? launch_f32_few<4>(a, plan, st)
-                                  : launch_f32_few<8>(a, plan, st);
+            : plan.unit_rows == 8 ? launch_f32_mma<1>(a, plan, st)
+                                  : launch_f32_mma<2>(a, plan, st);
     return e == cudaSuccess ? DEC_OK : rows_cuda_fail(who, e, "attention kernel launch");
 }
 

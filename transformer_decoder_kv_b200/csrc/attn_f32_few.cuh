@@ -23,8 +23,9 @@ namespace dec {
 constexpr int kF32Chunk = 16;
 constexpr int kF32Warps = 4;
 
+// (One row: five blocks per SM instead of four, 32 streams x 448 keys x 20 heads 30.6 -> 25.6 us; six spill.)
 template <int R>
-static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_few(const RowsAttnArgs a) {
+static __global__ void __launch_bounds__(kF32Warps * 32, R == 1 ? 5 : 4) k_attn_f32_few(const RowsAttnArgs a) {
     __shared__ float sm_m[kF32Warps][R], sm_l[kF32Warps][R];
     __shared__ __align__(16) float sm_o[kF32Warps][R][kHeadDim];
 

@@ -45,7 +45,7 @@ RowsPlan rows_shape(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, 
         p.warps = kFewWarps, p.chunk = kFewChunk, p.least = kFewWarps;
     } else {
         p.unit_rows = u <= 1 ? 1 : u <= 2 ? 2 : u <= 8 ? 8 : 16;
-        p.resident = u <= 2 ? 4 : 2;
+        p.resident = u <= 1 ? 5 : u <= 2 ? 4 : 2;
         p.warps = kF32Warps, p.chunk = kF32Chunk, p.least = 2 * kF32Warps;
     }
     p.tiles = (u + p.unit_rows - 1) / p.unit_rows;
@@ -91,7 +91,7 @@ size_t rows_workspace(const RowsPlan& p, const dec_kv_rows& rows, int n_heads) {
 template <int UR, int CK>
 cudaError_t launch_merge(const RowsAttnArgs& a, const RowsPlan& p, cudaStream_t st) {
     if (p.S == 1) return cudaSuccess;
-    return rows_launch(k_attn_merge<UR, CK>, dim3((a.r.max_rows + 3) / 4, a.heads, a.r.batch), 128, 0, st, a);
+    return rows_launch(k_attn_merge<UR, CK>, dim3((a.r.max_rows + 7) / 8, a.heads, a.r.batch), 128, 0, st, a);
 }
 
 template <typename K>

@@ -116,15 +116,14 @@ inline long long rows_max_chunks(const KvViewDev& v, long long rows, int window,
     return c < whole ? (c < 1 ? 1 : c) : whole;
 }
 
-// Joins the splits' partial states of each (row, head): one warp each, 16 bytes a lane, its halves
-// taking every other split. The states' loads are independent of each other (maximum and sums first
-// fetched together with the values), so a row costs about one round trip per eight splits.
+// Joins the splits' partial states of each (row, head): a half-warp each, 16 bytes a lane. Eight splits'
+// states are fetched at once, so a row costs about one round trip per eight splits.
 template <int UR, int CK>
 static __global__ void __launch_bounds__(128) k_attn_merge(const RowsAttnArgs a) {
     pdl_wait();
-    const int lane = threadIdx.x & 31, half = lane >> 4, d4 = lane & 15;
+    const int d4 = threadIdx.x & 15;
     const StreamRows s = stream_rows(a.r, a.v, blockIdx.z);
-    const int i = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y;
+    const int i = blockIdx.x * 8 + (threadIdx.x >> 4), h = blockIdx.y;
     if (i >= s.n) return;
     const UnitKeys k = unit_keys<UR, CK>(a, s, (i * a.group + h % a.group) / UR);
     if (k.splits <= 1) return;
@@ -132,31 +131,30 @@ static __global__ void __launch_bounds__(128) k_attn_merge(const RowsAttnArgs a)
     const float* p = a.part + (row * a.heads + h) * a.S * kPartStride;
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int sp0 = half; sp0 < k.splits; sp0 += 8) {
-        float2 ml[4];
-        float4 x[4];
+    for (int sp0 = 0; sp0 < k.splits; sp0 += 8) {
+        float2 ml[8];
+        float4 x[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             ml[j] = make_float2(-INFINITY, 0.0f);
             x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const int sp = sp0 + 2 * j;
-            if (sp < k.splits) {
-                ml[j] = __ldcg(reinterpret_cast<const float2*>(p + sp * kPartStride));
-                x[j] = __ldcg(reinterpret_cast<const float4*>(p + sp * kPartStride + 4) + d4);
+            if (sp0 + j < k.splits) {
+                ml[j] = __ldcg(reinterpret_cast<const float2*>(p + (sp0 + j) * kPartStride));
+                x[j] = __ldcg(reinterpret_cast<const float4*>(p + (sp0 + j) * kPartStride + 4) + d4);
             }
         }
         float mn = m;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mn = fmaxf(mn, ml[j].x);
+        for (int j = 0; j < 8; ++j) mn = fmaxf(mn, ml[j].x);
         const float corr = m == -INFINITY ? 0.0f : exp2f(m - mn);
         m = mn;
         l *= corr;
         o.x *= corr, o.y *= corr, o.z *= corr, o.w *= corr;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             const float w = ml[j].x == -INFINITY ? 0.0f : exp2f(ml[j].x - m);
-            l = fmaf(w, ml[j].y, l);
-            if (w != 0.0f) {      // a split without weight adds nothing, whatever its values are
+            l = fmaf(w, ml[j].y, l);   // (a sum that is not a number stays one)
+            if (w != 0.0f) {           // a split without weight adds nothing, whatever its values are
                 o.x = fmaf(w, x[j].x, o.x);
                 o.y = fmaf(w, x[j].y, o.y);
                 o.z = fmaf(w, x[j].z, o.z);
@@ -164,20 +162,9 @@ static __global__ void __launch_bounds__(128) k_attn_merge(const RowsAttnArgs a)
             }
         }
     }
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, 16), mx = fmaxf(m, m2);
-    const float w = m == -INFINITY ? 0.0f : exp2f(m - mx);
-    auto join = [&](float v) {
-        v = w == 0.0f ? 0.0f : v * w;
-        return v + __shfl_xor_sync(0xffffffffu, v, 16);
-    };
-    // a sum that is not a number stays one, also where it is all that its half has seen (w = 0)
-    l *= w;
-    l += __shfl_xor_sync(0xffffffffu, l, 16);
-    o.x = join(o.x), o.y = join(o.y), o.z = join(o.z), o.w = join(o.w);
     const bool ok = l > 0.0f && isfinite(l);
-    if (half == 0)
-        *(reinterpret_cast<float4*>(a.out + row * a.out_ld + h * kHeadDim) + d4) =
-            ok ? make_float4(o.x / l, o.y / l, o.z / l, o.w / l) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    *(reinterpret_cast<float4*>(a.out + row * a.out_ld + h * kHeadDim) + d4) =
+        ok ? make_float4(o.x / l, o.y / l, o.z / l, o.w / l) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
 
 }  // namespace dec

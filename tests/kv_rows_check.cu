@@ -77,7 +77,7 @@ static int check_units() {
 }
 
 int main() {
-    if (check_units<4, 64>() || check_units<16, 64>() || check_units<8, 16>() || check_units<1, 16>() || check_units<128, 128>()) return 1;
+    if (check_units<4, 64>() || check_units<16, 64>() || check_units<8, 16>() || check_units<16, 16>() || check_units<1, 16>() || check_units<128, 128>()) return 1;
     const int shapes[][4] = {{16, 3, 4, 12}, {32, 1, 1, 1}, {64, 7, 5, 40}, {300, 1, 6, 6}, {16, 130000, 900, 5}};
     for (const auto& sh : shapes) {
         for (int paged = 0; paged < 2; ++paged) {

@@ -119,7 +119,7 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const Ro
     // ---- running state: unit rows 8 nt + 2 t + b; O^T dims 8 g + 2 mt, + 1 ----
     float m[NT][2], rf[NT][2], l[NT][2], o[NT][4][4];       // maximum, reference of the weights, sum, values
     int ek = -100, E = -100;                       // K is held times 2^(10 - ek), V times 2^(10 - E)
-    float kscale = 0.0f;                           // 2^(ek - 10)
+    float kscale = __uint_as_float(static_cast<uint32_t>(127 - 110) << 23);      // 2^(ek - 10)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll

@@ -147,7 +147,7 @@ dec_status attn_rows(const char* who, const dec_kv_view* view, const dec_kv_rows
     RowsPlan plan{};
     if (!bad) {
         plan = rows_shape(KV4, *view, *rows, n_heads);
-        if (workspace_bytes < rows_workspace(plan, *rows, n_heads)) bad = "workspace too small";
+        if (workspace_bytes < dec_attention_rows_workspace_size(view, rows, n_heads)) bad = "workspace too small";
         if (plan.tiles * view->n_kv_heads > 65535) bad = "max_rows * n_heads is too large";
     }
     if (bad) return rows_fail(who, DEC_EINVAL, bad);

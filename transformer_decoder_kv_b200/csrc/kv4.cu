@@ -147,7 +147,6 @@ __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const 
     const unsigned mask = 0xffu << (threadIdx.x & 24);
     const int part = v.page_rows * kKv4RowBytes;
     const unsigned page_bytes = static_cast<unsigned>(v.heads) * 2u * part;
-    const long long cap = kv_capacity(v);
     F8 x[kTasks][2];
     float* src[kTasks][2];                         // null: no such row
     unsigned char* blk[kTasks];                    // null: no place, nothing to store or zeros to read
@@ -159,13 +158,9 @@ __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const 
         blk[i] = nullptr;
         src[i][0] = nullptr;
         if (row >= s.n) continue;                  // (8 lanes alike)
-        const long long pos = s.pos0 + row;
-        if (s.slot >= 0 && pos >= 0 && pos < cap) {
-            const int page = kv_page(v, s.slot, static_cast<int>(pos) >> v.shift);
-            pr[i] = static_cast<int>(pos) & (v.page_rows - 1);
-            if (page >= 0)
-                blk[i] = cache + static_cast<unsigned long long>(static_cast<unsigned>(page)) * page_bytes + head * (2 * part);
-        }
+        int page = 0;
+        if (kv_place(v, s, row, page, pr[i]))
+            blk[i] = cache + static_cast<unsigned long long>(static_cast<unsigned>(page)) * page_bytes + head * (2 * part);
         if (WRITE && !blk[i]) continue;
         const long long off = static_cast<long long>(s.row0 + row) * ld + (head * kHeadDim + l8 * 8);
         src[i][0] = k + off;

@@ -57,29 +57,41 @@ RowsPlan rows_shape(bool kv4, const dec_kv_view& view, const dec_kv_rows& rows, 
     return p;
 }
 
-// Splits: the fewest (waves of resident blocks) x (rounds of chunks per block, and its start and end),
-// a merge counting as one more round. Of the tensor-core splits within a tenth of the best the finest
-// is taken; where they make more than one wave their length is fixed, so that the blocks of short and
-// long streams are alike (in one wave a short stream is rather split as often as it can be).
+// Splits: the fewest (waves of resident blocks) x (rounds of chunks per block, and its start and end), a
+// merge counting as one more round. For the tensor-core tiles, whose blocks are few and long:
+//   - a batch whose n_rows falls short of batch * max_rows has about as many units as its rows fill, and
+//     their blocks differ in length, so its waves are counted in parts (16 chunks of 5 to 128 rows over 513
+//     to 4129 keys: 63 us, where whole waves of full streams had given 5 splits and 69 us; 4 would take 60);
+//   - elsewhere of the splits within a tenth of the best the finest is taken;
+//   - where the splits make more than one wave their length is fixed, so that the blocks of short and long
+//     streams are alike (in one wave a short stream is rather split as often as it can be).
 void rows_splits(RowsPlan& p, const dec_kv_view& view, const dec_kv_rows& rows, int window, int sinks) {
     const long long span = std::min<long long>(rows.max_rows, p.unit_rows / p.group + 1);
     const int chunks = static_cast<int>(rows_max_chunks(view_dev(view), span, window, sinks, p.chunk));
     const int most = std::max(1, std::min(p.most_splits, chunks / p.least));
-    const unsigned slots = kRowsSms * p.resident, start = p.tc ? 2 : 1;
-    auto cost = [&](unsigned S) {
-        const unsigned rounds = ((chunks + S - 1) / S + p.warps - 1) / p.warps;
-        return (static_cast<unsigned long long>(p.units) * S + slots - 1) / slots * (rounds + start) + (S > 1);
+    const long long slots = static_cast<long long>(kRowsSms) * p.resident, start = p.tc ? 2 : 1;
+    long long units = p.units;
+    bool parts = false;
+    if (p.tc && rows.batch > 1) {
+        const long long filled = view.n_kv_heads * (static_cast<long long>(rows.n_rows) * p.group / p.unit_rows + rows.batch / 2);
+        parts = 10 * filled < 9 * units;
+        if (parts) units = std::max(1ll, filled);
+    }
+    auto cost = [&](long long S) {                 // in sixteenths of a round
+        const long long rounds = ((chunks + S - 1) / S + p.warps - 1) / p.warps + start;
+        const long long waves = parts ? 16 * std::max(slots, units * S) / slots : (units * S + slots - 1) / slots * 16;
+        return waves * rounds + (S > 1 ? 16 : 0);
     };
     p.S = 1;
-    unsigned long long best = most > 1 ? cost(1) : 0;
+    long long best = most > 1 ? cost(1) : 0;
     for (int S = 2; S <= most; ++S) {
-        const unsigned long long c = cost(S);
+        const long long c = cost(S);
         if (c < best) best = c, p.S = S;
     }
-    if (p.tc)
+    if (p.tc && !parts)
         for (int S = most; S > p.S; --S)
             if (10 * cost(S) <= 11 * best) p.S = S;
-    p.per_split = !p.tc ? p.least : p.units * p.S <= slots ? 2 : (chunks + p.S - 1) / p.S;
+    p.per_split = !p.tc ? p.least : units * p.S <= slots ? 2 : (chunks + p.S - 1) / p.S;
 }
 
 size_t rows_workspace(const RowsPlan& p, const dec_kv_rows& rows, int n_heads) {

@@ -199,8 +199,7 @@ def _pages(case, i, b_slot, cap_pages):
 def _quantise(x):
     """Codes and scales of f32 rows [n, HK, 64], the quotient in 64 bits (values next to a border)."""
     g = x.view(x.shape[0], x.shape[1], D // GROUP, GROUP)
-    a = g.abs().amax(-1)
-    s = torch.div(a, torch.full_like(a, 7.0)).to(torch.bfloat16).float()     # a true quotient, not a * (1 / 7)
+    s = (g.abs().amax(-1) / 7.0).to(torch.bfloat16).float()
     s = torch.where(s < 2.0 ** -126, torch.zeros_like(s), s)
     q = torch.round(g.double() / torch.where(s > 0, s, torch.ones_like(s)).double().unsqueeze(-1))
     q = torch.where(s.unsqueeze(-1) > 0, q, torch.zeros_like(q)).clamp(-7, 7)
@@ -345,7 +344,7 @@ def _exact_values(x, heads):
     """What the 4-bit cache stands for, of f32 rows [n, heads * 64]."""
     y = x.to(torch.float64).reshape(-1, heads, 2, 32)
     a = y.abs().max(dim=3, keepdim=True).values
-    s = torch.div(a, torch.full_like(a, 7.0)).to(torch.float32).to(torch.bfloat16).to(torch.float64)
+    s = (a / 7.0).to(torch.float32).to(torch.bfloat16).to(torch.float64)
     live = s >= 2.0 ** -126
     codes = torch.where(live, (y / torch.where(live, s, torch.ones_like(s))).round(), torch.zeros_like(y))
     return (codes * torch.where(live, s, torch.zeros_like(s))).reshape(-1, heads, 64)

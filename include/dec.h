@@ -552,6 +552,16 @@ size_t dec_kv4_bytes(const dec_kv_view* view);
 dec_status dec_kv4_write(const dec_kv_view* view, const dec_kv_rows* rows, const float* k, const float* v, int64_t ld,
                          void* cache, void* stream);
 
+/*
+ * dec_kv4_write with the scale's rule: DEC_KV4_SCALE_QUOTIENT is dec_kv4_write's (a / 7 rounded to f32);
+ * DEC_KV4_SCALE_PRODUCT takes a times the f32 next to 1 / 7, rounded to f32, as tensor libraries evaluate
+ * a / 7.0 on a GPU (torch does), so that the codes and scales equal a cache quantised there. About one scale
+ * in 60,000 differs between the two, by one step of bf16.
+ */
+enum { DEC_KV4_SCALE_QUOTIENT = 0, DEC_KV4_SCALE_PRODUCT = 1 };
+dec_status dec_kv4_write_scaled(const dec_kv_view* view, const dec_kv_rows* rows, const float* k, const float* v,
+                                int64_t ld, void* cache, int32_t scale_rule, void* stream);
+
 /* Read the batch's rows back as f32 into k_out and v_out (device, the layout of dec_kv4_write). */
 dec_status dec_kv4_read(const dec_kv_view* view, const dec_kv_rows* rows, const void* cache, float* k_out,
                         float* v_out, int64_t ld, void* stream);

@@ -31,9 +31,10 @@ EXPORTS = ["dec_create", "dec_destroy", "dec_last_error", "dec_prefill", "dec_kv
            "dec_next_tokens", "dec_get_config", "dec_generate", "dec_set_prefill_chunk",
            "dec_set_phase_timing", "dec_phase_times", "dec_release_slot", "dec_kv_pages_free",
            "dec_attention_workspace_size", "dec_attention", "dec_attention_plan", "dec_attention_noalloc",
-           "dec_i8_dot", "dec_kv4_bytes", "dec_kv4_write", "dec_kv4_read",
+           "dec_i8_dot", "dec_kv4_bytes", "dec_kv4_write", "dec_kv4_write_scaled", "dec_kv4_read",
            "dec_attention_rows_workspace_size", "dec_attention_kv4", "dec_attention_window"]
 I8_PATH = {"dp4a": 0, "tcgen05": 1}
+KV4_SCALE = {"quotient": 0, "product": 1}
 DEC_INJECT_DROP_ATTN_COPY = 1
 PHASE_NAMES = {1: "embed", 2: "qkv", 3: "self_attn", 4: "o", 5: "cross_q", 6: "cross_attn", 7: "cross_o",
                8: "ffn_up", 9: "ffn_down", 10: "head"}
@@ -128,6 +129,7 @@ def load_library(path: str = LIB_PATH) -> C.CDLL:
         "dec_i8_dot": (C.c_int, [vp, vp, i32, i32, i32, i32, vp, vp]),
         "dec_kv4_bytes": (C.c_size_t, [vp]),
         "dec_kv4_write": (C.c_int, [vp, vp, vp, vp, C.c_int64, vp, vp]),
+        "dec_kv4_write_scaled": (C.c_int, [vp, vp, vp, vp, C.c_int64, vp, i32, vp]),
         "dec_kv4_read": (C.c_int, [vp, vp, vp, vp, vp, C.c_int64, vp]),
         "dec_attention_rows_workspace_size": (C.c_size_t, [vp, vp, i32]),
         "dec_attention_kv4": (C.c_int, [vp, vp, vp, C.c_int64, i32, vp, i32, i32, vp, C.c_int64, vp, C.c_size_t, vp]),
@@ -492,14 +494,22 @@ def kv4_bytes(view: KvView) -> int:
     return view.kv4_bytes
 
 
-def kv4_write(view: KvView, rows: KvRows, k, v, cache, stream: int = 0):
-    """Quantise and store the batch's K and V rows (f32 [n_rows, n_kv_heads * 64], any row stride)."""
+def kv4_write(view: KvView, rows: KvRows, k, v, cache, stream: int = 0, scale: str = "quotient"):
+    """Quantise and store the batch's K and V rows (f32 [n_rows, n_kv_heads * 64], any row stride).
+    scale: a group's max / 7 as the f32 "quotient", or as the "product" with the f32 next to 1 / 7, which is
+    what torch's max / 7.0 gives on a GPU."""
+    if scale not in KV4_SCALE:
+        _einval(f"dec_kv4_write_scaled: scale must be one of {sorted(KV4_SCALE)}, got {scale!r}")
     _same_device(view, rows)
     kp, ld = _rows_2d("k", k, rows, view.width)
     vp, ld_v = _rows_2d("v", v, rows, view.width)
     if ld != ld_v:
         _einval("dec_kv4_write: k and v have different row strides")
-    _raise_thread_error(lib().dec_kv4_write(view.ref, rows.ref, kp, vp, ld, _pool(view, rows, cache), stream))
+    pool = _pool(view, rows, cache)
+    if scale == "quotient":
+        _raise_thread_error(lib().dec_kv4_write(view.ref, rows.ref, kp, vp, ld, pool, stream))
+    else:
+        _raise_thread_error(lib().dec_kv4_write_scaled(view.ref, rows.ref, kp, vp, ld, pool, KV4_SCALE[scale], stream))
 
 
 def kv4_read(view: KvView, rows: KvRows, cache, k_out, v_out, stream: int = 0):

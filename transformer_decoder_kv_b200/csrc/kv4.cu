@@ -2,9 +2,10 @@
 // (dec_kv4_read).
 //
 // Per (row, K/V head, group of 32 dims): a = max |x|, s = bf16(a / 7), c = round(x / s) to the
-// nearest integer, ties to even; value c s. The scale is rounded before the codes are chosen, so
-// |x - c s| <= s / 2 holds whatever its rounding (a / s <= 7 (1 + 2^-8) rounds to 7), and bf16 keeps
-// f32's range. c s has 3 + 8 significant bits: exact in f32, and in f16 up to a power of two.
+// nearest integer, ties to even; value c s. a / 7 is the f32 quotient or a times the f32 next to 1 / 7, as the
+// call asks: next to a border of bf16 the two give neighbouring scales. The scale is rounded before the codes
+// are chosen, so |x - c s| <= s / 2 holds whatever its rounding (a / s <= 7 (1 + 2^-8 + 2^-22) rounds to 7),
+// and bf16 keeps f32's range. c s has 3 + 8 significant bits: exact in f32, and in f16 up to a power of two.
 //
 // The code is decided exactly: c0, the integer next to x * (1 / s) in f32, is within one of it, and
 // e = x - c0 s is exact in f32 (fma; c0 s has 11 significant bits and cancels x's leading ones;
@@ -55,7 +56,7 @@ __device__ __forceinline__ void store8(float* p, const F8& x) {
 }
 
 // Word of 8 codes + 8 and the bf16 bits of their scale, the group's four lanes together.
-__device__ __forceinline__ uint32_t kv4_quantise(const F8& x, unsigned mask, uint32_t& scale) {
+__device__ __forceinline__ uint32_t kv4_quantise(const F8& x, unsigned mask, bool product, uint32_t& scale) {
     float a = 0.0f;
     float2 z = make_float2(0.0f, 0.0f);            // 0 while everything is finite
 #pragma unroll
@@ -68,7 +69,7 @@ __device__ __forceinline__ uint32_t kv4_quantise(const F8& x, unsigned mask, uin
     a = fmaxf(a, __shfl_xor_sync(mask, a, 2));
     scale = 0x7fc0u;
     if (!(a < INFINITY)) return 0x88888888u;
-    const uint32_t u = __float_as_uint(__fdiv_rn(a, 7.0f));
+    const uint32_t u = __float_as_uint(product ? __fmul_rn(a, 1.0f / 7.0f) : __fdiv_rn(a, 7.0f));
     scale = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
     if (scale < 0x0080u) {
         scale = 0;
@@ -136,7 +137,7 @@ __device__ __forceinline__ F8 kv4_dequantise(uint32_t w, float s) {
 template <bool WRITE, bool WIDE>
 __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const KvRowsDev r, float* __restrict__ k,
                                                        float* __restrict__ vv, long long ld,
-                                                       unsigned char* __restrict__ cache, int lh) {
+                                                       unsigned char* __restrict__ cache, int lh, bool product) {
     pdl_wait();
     const StreamRows s = stream_rows(r, v, blockIdx.y);
     const int head_blocks = v.heads >> lh, row_block = blockIdx.x / head_blocks;
@@ -180,8 +181,8 @@ __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const 
             unsigned char* codes = blk[i] + pr[i] * 32;
             unsigned char* scale = blk[i] + sw + pr[i] * 4;
             uint32_t sk, sv;
-            *reinterpret_cast<uint32_t*>(codes + kw) = kv4_quantise(x[i][0], mask, sk);
-            const uint32_t w = kv4_quantise(x[i][1], mask, sv);
+            *reinterpret_cast<uint32_t*>(codes + kw) = kv4_quantise(x[i][0], mask, product, sk);
+            const uint32_t w = kv4_quantise(x[i][1], mask, product, sv);
             *reinterpret_cast<uint32_t*>(codes + vw) = ((w << 2) & 0xfffcfffcu) | ((w >> 14) & 0x00030003u);
             if ((l8 & 3) == 0) {
                 *reinterpret_cast<uint16_t*>(scale) = static_cast<uint16_t>(sk);
@@ -213,13 +214,14 @@ __global__ void __launch_bounds__(kThreads) k_kv4_rows(const KvViewDev v, const 
 
 template <bool WRITE>
 dec_status kv4_rows(const char* who, const dec_kv_view* view, const dec_kv_rows* rows, float* k, float* v, int64_t ld,
-                    unsigned char* cache, void* stream) {
+                    unsigned char* cache, int32_t scale_rule, void* stream) {
     const char* bad = view_problem(view, true);
     if (!bad) bad = rows_problem(rows);
     if (!bad && (!k || !v || !cache)) bad = "null pointer";
     if (!bad && (ld < static_cast<int64_t>(view->n_kv_heads) * kHeadDim || (ld & 3)))
         bad = "ld must be a multiple of 4 and at least n_kv_heads * 64";
     if (!bad && !(aligned16(k) && aligned16(v) && aligned16(cache))) bad = "k, v and cache must be 16-byte aligned";
+    if (!bad && scale_rule != DEC_KV4_SCALE_QUOTIENT && scale_rule != DEC_KV4_SCALE_PRODUCT) bad = "unknown scale_rule";
     if (bad) return rows_fail(who, DEC_EINVAL, bad);
     int lh = 0;
     while (lh < 4 && view->n_kv_heads % (2 << lh) == 0) ++lh;
@@ -230,7 +232,7 @@ dec_status kv4_rows(const char* who, const dec_kv_view* view, const dec_kv_rows*
     const cudaError_t e = rows_launch(wide ? k_kv4_rows<WRITE, true> : k_kv4_rows<WRITE, false>,
                                       dim3(static_cast<unsigned>(blocks), rows->batch), kThreads, 0,
                                       static_cast<cudaStream_t>(stream), view_dev(*view), rows_dev(*rows), k, v,
-                                      static_cast<long long>(ld), cache, lh);
+                                      static_cast<long long>(ld), cache, lh, scale_rule == DEC_KV4_SCALE_PRODUCT);
     if (e != cudaSuccess) return rows_cuda_fail(who, e, "k_kv4_rows launch");
     return DEC_OK;
 }
@@ -247,13 +249,19 @@ size_t dec_kv4_bytes(const dec_kv_view* view) {
 dec_status dec_kv4_write(const dec_kv_view* view, const dec_kv_rows* rows, const float* k, const float* v, int64_t ld,
                          void* cache, void* stream) {
     return kv4_rows<true>("dec_kv4_write", view, rows, const_cast<float*>(k), const_cast<float*>(v), ld,
-                          static_cast<unsigned char*>(cache), stream);
+                          static_cast<unsigned char*>(cache), DEC_KV4_SCALE_QUOTIENT, stream);
+}
+
+dec_status dec_kv4_write_scaled(const dec_kv_view* view, const dec_kv_rows* rows, const float* k, const float* v,
+                                int64_t ld, void* cache, int32_t scale_rule, void* stream) {
+    return kv4_rows<true>("dec_kv4_write_scaled", view, rows, const_cast<float*>(k), const_cast<float*>(v), ld,
+                          static_cast<unsigned char*>(cache), scale_rule, stream);
 }
 
 dec_status dec_kv4_read(const dec_kv_view* view, const dec_kv_rows* rows, const void* cache, float* k_out,
                         float* v_out, int64_t ld, void* stream) {
     return kv4_rows<false>("dec_kv4_read", view, rows, k_out, v_out, ld,
-                           static_cast<unsigned char*>(const_cast<void*>(cache)), stream);
+                           static_cast<unsigned char*>(const_cast<void*>(cache)), DEC_KV4_SCALE_QUOTIENT, stream);
 }
 
 }  // extern "C"

@@ -234,7 +234,7 @@ def prepare(case, seed):
             st["cache"] = torch.zeros(pkg.kv4_bytes(st["view"]), dtype=torch.uint8, device=DEV)
         if case["op"] in ("kv4_read", "attention_kv4"):
             every = pkg.KvRows(B, dev(lens), i["slots"], dev(_starts(lens)), sum(lens), max(lens))
-            pkg.kv4_write(st["view"], every, i["k"], i["v"], st["cache"])
+            pkg.kv4_write(st["view"], every, i["k"], i["v"], st["cache"], scale="product")
         if case["op"] in ("attention_kv4", "attention_window"):
             nb = pkg.attention_rows_workspace_size(st["view"], st["batch"], H)
             st["ws"] = torch.zeros((nb + 3) // 4, dtype=torch.int32, device=DEV)
@@ -272,7 +272,7 @@ def prepare(case, seed):
 def _run_own(st):
     case, pkg, i = st["case"], st["pkg"], st["i"]
     if case["op"] == "kv4_write":
-        pkg.kv4_write(st["view"], st["batch"], i["k"], i["v"], st["cache"])
+        pkg.kv4_write(st["view"], st["batch"], i["k"], i["v"], st["cache"], scale="product")
         pkg.kv4_read(st["view"], st["batch"], st["cache"], st["ko"], st["vo"])
         return st["ko"], st["vo"]
     if case["op"] == "kv4_read":

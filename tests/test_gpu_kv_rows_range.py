@@ -1,0 +1,91 @@
+"""The row-batch attentions over values of very different size: keys that some or all rows do not see,
+keys without weight, tiles that are not finite, lengths past a slot's end.
+
+Tolerance of a row (`_reference`), every term a bound of one step: scores are off by 2^-18 of sum |q k| / 8 at
+most (operands carried to 22 bits, 3 2^-22, and 64 terms in three products summed in f32), a key's own and the
+maximum's; values by 3 2^-22 (two operands of 22 bits, the product of the low parts left out) and sums over
+keys by 2^-23 per step of 16 keys or more, all of them relative to sum p |v|; a weight below f16's range is
+off by 2^-37 of the largest.
+"""
+import numpy as np
+import pytest
+
+from tests._kvrows import D, Setup, check, kv4_values
+
+pytestmark = pytest.mark.gpu
+
+# rows of one stream with one head: each of the kernels
+KINDS = [(True, 1), (True, 6), (True, 12), (True, 100), (False, 1), (False, 2), (False, 5), (False, 20), (False, 100)]
+SHARED = [k for k in KINDS if k[1] > 2]
+_id = lambda k: f"{'kv4' if k[0] else 'f32'}-{k[1]}" if isinstance(k, tuple) else None
+
+
+def _stream(kind, n, page_rows=16, seed=3):
+    kv4, r = kind
+    s = Setup(1, 1, [n], [r], page_rows, False, seed=seed, spare_slots=0, pad_rows=0)
+    s.v[0] *= np.float32(0.5)
+    return s
+
+
+def _reference(s, kv4, window, sinks, pos=None):
+    k, v = (kv4_values(x[0]) if kv4 else x[0] for x in (s.k, s.v))
+    k, v = np.asarray(k, np.float64)[:, 0], np.asarray(v, np.float64)[:, 0]
+    r, j = s.rows[0], np.arange(len(k))
+    pos = np.arange(s.lens[0] - r, s.lens[0]) if pos is None else pos
+    out, tol = np.zeros((r, D)), np.zeros((r, 1))
+    for i, p in enumerate(pos):
+        see = (j <= p) & ((j > p - window) | (j < sinks)) if window else j <= p
+        kk, vv, q = k[see], v[see], s.q[i, 0].astype(np.float64)
+        with np.errstate(all="ignore"):
+            x = kk @ q / 8
+            w = np.exp(x - x.max()) if len(x) else x
+            if not (len(w) and np.isfinite(w.sum()) and w.sum() > 0):
+                continue
+            w = w / w.sum()
+            out[i] = np.where(w[:, None] == 0, 0, w[:, None] * vv).sum(0)
+            live = w > 1e-40                        # e^-92: far below the smallest weight that counts
+            amp = np.abs(np.where(np.isfinite(kk), kk, 0) * q)[live].sum(1).max() / 8
+            mass = np.where(np.isfinite(vv), np.abs(vv), 0)[live]
+            tol[i] = ((w[live, None] * mass).sum(0).max() * (2 * 2.0 ** -18 * amp + 3 * 2.0 ** -22 + (len(w) / 16 + 32) * 2.0 ** -23)
+                      + mass.max() * 2.0 ** -37 * live.sum())
+    return out, tol
+
+
+def _caches(s, kv4):
+    if not kv4:
+        return s.f32_pools()
+    c = s.new_cache()
+    s.write_all(c)
+    return c
+
+
+def _check(s, kv4, window=0, sinks=0, caches=None):
+    out = s.attend(kv4, window, sinks, _caches(s, kv4) if caches is None else caches)
+    s.torch.cuda.synchronize()
+    ref, tol = _reference(s, kv4, window, sinks)
+    check(out.cpu().numpy(), ref, tol)
+
+
+@pytest.mark.parametrize("value", [1e12, -1e30, 3e38])
+@pytest.mark.parametrize("kind", KINDS, ids=_id)
+def test_large_values_that_no_row_sees(kind, value):
+    """Behind the window and past the sinks, the border chunks of both among them."""
+    s = _stream(kind, 300)
+    s.k[0][4:300 - kind[1] - 40 + 1, 0, ::5] = value
+    s.v[0][4:300 - kind[1] - 40 + 1, 0, 3::7] = value
+    _check(s, kind[0], 40, 4)
+
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("rows", [1, 4, 8, 16, 100])
+def test_rows_never_written_hold_anything(rows, seed):
+    """Every bit pattern of codes and scales outside the rows that are seen."""
+    s = _stream((True, rows), 300, seed=seed)
+    t = s.torch
+    g = t.Generator(device="cuda").manual_seed(seed)
+    cache = t.randint(0, 256, (s.pkg.kv4_bytes(s.view),), dtype=t.uint8, device="cuda", generator=g)
+    lo, sinks = 300 - rows - 40 + 1, 4
+    one = lambda a, n: s.f32(a[0][a_lo:a_lo + n].reshape(n, D))
+    for a_lo, n in ((0, sinks), (lo, 300 - lo)):
+        s.pkg.kv4_write(s.view, s.make_rows([a_lo + n], [n]), one(s.k, n), one(s.v, n), cache)
+    _check(s, True, 40, sinks, cache)

@@ -273,6 +273,8 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
     // chunks whose 64 keys all rows see: below, and above or within the sinks
     const int full_hi = static_cast<int>(min(p_first - (kFewChunk - 1), 0x7fffff00ll));
     const int full_lo = a.window == 0 ? 0 : static_cast<int>(max(0ll, min(p_last - a.window + 1, 0x7fffff00ll)));
+    // keys below, past the sinks: no row sees them
+    const int seen_lo = a.window > 0 ? static_cast<int>(max(0ll, min(p_first - a.window + 1, 0x7fffff00ll))) : 0;
     const int key_a = (g >> 1) + 4 * (g & 1);           // key of S^T row g of a 16-key half
 
     int stage = 0;
@@ -306,9 +308,10 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
             }
         }
 
-        // V scales, lane = two keys 4 apart: f16 of 16 times scale 2^(9 - E), 0 for keys without a page
-        // or row, and for a scale that is not a number (those keys' outputs are set below). Kept in
-        // the order their readers want: keys 16 i + t, + 4, + 8, + 12 of quad lane t side by side.
+        // V scales, lane = two keys 4 apart: f16 of 16 times scale 2^(9 - E), 0 for keys that no row sees
+        // (whose bits may be anything), and for a scale that is not a number (those keys' outputs are
+        // set below). Kept in the order their readers want: keys 16 i + t, + 4, + 8, + 12 of quad lane t
+        // side by side. (A row never written may hold a negative scale: magnitudes are compared.)
         float fac = 1.0f;
         uint32_t any_nan;
         const int vkey = (lane >> 3) * 16 + ((lane >> 1) & 3) + 8 * (lane & 1);
@@ -319,21 +322,26 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
             for (int w = 0; w < 2; ++w) {
                 const int key = vkey + 4 * w;
                 vw[w] = *reinterpret_cast<const uint32_t*>(st + kFewVs + key * 4);
-                if (!full && ((((lane & 16) ? have[1] : have[0]) >> (key & 31) & 1u) == 0u || j0 + key > p_last)) vw[w] = 0;
+                if (!full) {
+                    const int j = j0 + key;
+                    const bool seen = (((lane & 16) ? have[1] : have[0]) >> (key & 31) & 1u) && j <= p_last &&
+                                      (j >= seen_lo || j < a.sinks);
+                    vw[w] = seen ? vw[w] : 0u;
+                }
                 z[w][0] = __uint_as_float(vw[w] << 16);
                 z[w][1] = __uint_as_float(vw[w] & 0xffff0000u);
-                big = fmaxf(big, fmaxf(z[w][0], z[w][1]));
+                big = fmaxf(big, fmaxf(fabsf(z[w][0]), fabsf(z[w][1])));
             }
             // (stored scales are below 2^126: four of them stay finite)
-            any_nan = __ballot_sync(0xffffffffu, !((z[0][0] + z[0][1]) + (z[1][0] + z[1][1]) < INFINITY));
+            any_nan = __ballot_sync(0xffffffffu, !((fabsf(z[0][0]) + fabsf(z[0][1])) + (fabsf(z[1][0]) + fabsf(z[1][1])) < INFINITY));
             if (any_nan) {
                 big = 0.0f;
 #pragma unroll
                 for (int w = 0; w < 2; ++w)
 #pragma unroll
                     for (int gr = 0; gr < 2; ++gr) {
-                        if (!(z[w][gr] < INFINITY)) z[w][gr] = 0.0f;
-                        big = fmaxf(big, z[w][gr]);
+                        if (!(fabsf(z[w][gr]) < INFINITY)) z[w][gr] = 0.0f;
+                        big = fmaxf(big, fabsf(z[w][gr]));
                     }
             }
             const int e = max(static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23) - 127, -100);

@@ -89,3 +89,17 @@ def test_rows_never_written_hold_anything(rows, seed):
     for a_lo, n in ((0, sinks), (lo, 300 - lo)):
         s.pkg.kv4_write(s.view, s.make_rows([a_lo + n], [n]), one(s.k, n), one(s.v, n), cache)
     _check(s, True, 40, sinks, cache)
+
+
+@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("page_rows", [37, 100, 129])
+@pytest.mark.parametrize("kind", [k for k in KINDS if not k[0] and k[1] < 37], ids=_id)
+def test_queries_past_the_end_of_a_slot_of_any_size(kind, page_rows, window):
+    s = _stream(kind, page_rows, page_rows)
+    caches = s.f32_pools()
+    for past in (1, 8, 20):
+        s.batch = s.make_rows([page_rows + past], s.rows)
+        out = s.attend(False, window, 0, caches)
+        s.torch.cuda.synchronize()
+        ref, tol = _reference(s, False, window, 0, np.arange(page_rows + past - kind[1], page_rows + past))
+        check(out.cpu().numpy(), ref, tol, past)

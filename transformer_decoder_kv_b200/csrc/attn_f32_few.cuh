@@ -92,7 +92,7 @@ static __global__ void __launch_bounds__(kF32Warps * 32, R == 1 ? 5 : 4) k_attn_
     load(vv, a.vv, at, c);
     for (; c < c_end; c += kF32Warps) {
         const int j0 = unit_chunk(k, c) * kF32Chunk;
-        const bool full = at >= 0 && j0 <= full_hi && (j0 >= full_lo || j0 + kF32Chunk <= a.sinks);
+        const bool full = at >= 0 && j0 <= full_hi && j0 + kF32Chunk <= end && (j0 >= full_lo || j0 + kF32Chunk <= a.sinks);
         float sc[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {

@@ -103,3 +103,18 @@ def test_queries_past_the_end_of_a_slot_of_any_size(kind, page_rows, window):
         s.torch.cuda.synchronize()
         ref, tol = _reference(s, False, window, 0, np.arange(page_rows + past - kind[1], page_rows + past))
         check(out.cpu().numpy(), ref, tol, past)
+
+
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("value", [np.float32(63.99), np.float32(65535) / 1024])
+@pytest.mark.parametrize("rows", [20, 100])
+def test_values_just_below_a_power_of_two(rows, value, what):
+    """Tiles of values below 2, and one of a later tile whose size in f16 would round up to infinity."""
+    s = _stream((False, rows), 900)
+    for x in (s.k, s.v):
+        np.clip(x[0], -1.9, 1.9, out=x[0])
+        x[0][:, 0, 0] = 1.5
+    for at in (200, 330, 600):
+        (s.k if what == "k" else s.v)[0][at, 0, 9] = value
+    s.q[:, 0, 9] *= np.float32(0.05)
+    _check(s, False)

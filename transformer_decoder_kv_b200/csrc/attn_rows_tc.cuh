@@ -391,16 +391,17 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             fence_async_smem();
             __syncthreads();
         } else {
-            // The powers of two stand while the values stay within 2^6 of the largest one met when they
-            // were set; a tile beyond them (the first one, to begin with) sets them anew.
+            // The powers of two stand while the values, held below 2^11 when they were set, stay below 2^15
+            // (2^16 itself would not do: f16 ends at 65504); a tile beyond them (the first one, to begin
+            // with) sets them anew.
             float4 x[8];
             load_f32(c, entry, a.k, x);
             uint32_t km = magnitude(x);
             store_f32(sK, x, pow2i(10 - ek));
             load_f32(c, entry, a.vv, vf);
             uint32_t vm = magnitude(vf);
-            const uint32_t klim = static_cast<uint32_t>(min(127 + ek + 6, 255)) << 23;
-            const uint32_t vlim = static_cast<uint32_t>(min(127 + E + 6, 255)) << 23;
+            const uint32_t klim = static_cast<uint32_t>(min(127 + ek + 5, 255)) << 23;
+            const uint32_t vlim = static_cast<uint32_t>(min(127 + E + 5, 255)) << 23;
             fence_async_smem();
             if (__syncthreads_or(c == c0 || km >= klim || vm >= vlim)) {
                 km = __reduce_max_sync(0xffffffffu, km);

@@ -118,3 +118,22 @@ def test_values_just_below_a_power_of_two(rows, value, what):
         (s.k if what == "k" else s.v)[0][at, 0, 9] = value
     s.q[:, 0, 9] *= np.float32(0.05)
     _check(s, False)
+
+
+@pytest.mark.parametrize("flat", [False, True], ids=["scaled", "flat"])
+@pytest.mark.parametrize("kind", [k for k in SHARED if k[1] < 64], ids=_id)
+def test_a_first_tile_that_is_not_finite(kind, flat):
+    """NaN in the last row's own key: the rows before it, with values of 1000 or weights all alike, do not see it."""
+    kv4, r = kind
+    for n in (r + 3, r + 60):
+        s = _stream(kind, n)
+        if flat:
+            s.q[:] = 0
+            s.v[0][:] = 1
+        else:
+            s.v[0] *= np.float32(1000)
+        s.v[0][n - 1, 0, 3] = np.nan
+        s.k[0][n - 2, 0, 5] = np.inf
+        if flat:
+            s.k[0][n - 2, 0, 5] = 1.0
+        _check(s, kv4)

@@ -16,13 +16,16 @@
 //
 // The powers of two of K and V stand while the values stay within f16's range; a chunk beyond them (the
 // first one, to begin with) sets them anew. A chunk that holds a NaN or an infinity is computed by a plain
-// f32 loop: in a matrix product it would reach rows that do not see it.
+// f32 loop: in a matrix product it would reach rows that do not see it. From such a chunk on the sums are
+// kept in a scale of their own, 2^-16, in which f32 holds those of all finite values.
 #pragma once
 
 #include "attn_f32_few.cuh"
 #include "attn_kv4_few.cuh"
 
 namespace dec {
+
+constexpr int kMmaOwnScale = 26;           // o is held times 2^(10 - 26)
 
 template <int NT>
 static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const RowsAttnArgs a) {
@@ -119,6 +122,7 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const Ro
     // ---- running state: unit rows 8 nt + 2 t + b; O^T dims 8 g + 2 mt, + 1 ----
     float m[NT][2], rf[NT][2], l[NT][2], o[NT][4][4];       // maximum, reference of the weights, sum, values
     int ek = -100, E = -100;                       // K is held times 2^(10 - ek), V times 2^(10 - E)
+    bool own = false;                              // o is held times 2^-16, or else as V
     float kscale = __uint_as_float(static_cast<uint32_t>(127 - 110) << 23);      // 2^(ek - 10)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -209,7 +213,7 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const Ro
             if (!plain) {
                 ek = max(ek, static_cast<int>(km >> 23) - 127);
                 const int e = max(E, static_cast<int>(vm >> 23) - 127);
-                fac = E < e - 120 ? 0.0f : pow2(E - e);
+                if (!own) fac = E < e - 120 ? 0.0f : pow2(E - e);
                 E = e;
                 kscale = pow2(ek - 10);
                 convert();
@@ -279,6 +283,11 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const Ro
                     mma_f16(d, vl[mt], ph[nt][0], ph[nt][1], 0.0f, 0.0f, 0.0f, 0.0f);
                     mma_f16(d, vh[mt], pl[nt][0], pl[nt][1]);
                     mma_f16(d, vh[mt], ph[nt][0], ph[nt][1]);
+                    if (own) {
+                        const float df = pow2(E - kMmaOwnScale);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) d[j] *= df;
+                    }
 #pragma unroll
                     for (int j = 0; j < 4; j += 2) {
                         const float2 y = fma2(make_float2(o[nt][mt][j], o[nt][mt][j + 1]), make_float2(corr[nt][0], corr[nt][1]),
@@ -289,7 +298,16 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const Ro
                 }
         } else {
             // ---- plain loop: every quad lane takes all keys of its rows, lanes g = 0 their sums ----
-            const float vs = pow2(10 - E);
+            const float vs = pow2(10 - kMmaOwnScale);
+            if (!own) {
+                own = true;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[nt][mt][j] *= pow2(E - kMmaOwnScale);
+            }
             for (int x = 0; x < kF32Chunk; ++x) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -328,7 +346,7 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const Ro
     }
 
     // ---- join the warps ----
-    const float back = pow2(E - 10);
+    const float back = pow2((own ? kMmaOwnScale : E) - 10);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

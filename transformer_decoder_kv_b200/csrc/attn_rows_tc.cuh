@@ -24,7 +24,8 @@
 // the issue, a queue of work on the device and 96 registers for more warps were all slower.
 //
 // A tile that holds a NaN or an infinity in K or V, at a position that some row sees, is computed by a
-// plain f32 loop instead: in a matrix product it would reach the rows that do not see it.
+// plain f32 loop instead: in a matrix product it would reach the rows that do not see it. From such a tile
+// on the sums are kept in a scale of their own, 2^-16, in which f32 holds those of all finite values.
 #pragma once
 
 #include "attn_kv4_few.cuh"
@@ -267,12 +268,16 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
     constexpr int vbits = KV4 ? 9 : 10;
+    constexpr int own_scale = vbits + 16;
     int ek = -100, E = -100;                       // K is held times 2^(10 - ek), V times 2^(vbits - E)
-    float fac = 1.0f;                              // what the last change of E makes of O
-    auto raise_E = [&](int e) {
-        const int n = max(E, e);
-        fac = E < n - 120 ? 0.0f : pow2i(E - n);
+    bool own = false;                              // O is held times 2^-16, or else as V
+    float fac = 1.0f, df = 1.0f;                   // what the last change of scale makes of O, and P V's scale
+    auto set_scale = [&](int e, bool plain) {
+        const int n = plain ? E : max(E, e);
+        if (!own) fac = plain ? pow2i(E - own_scale) : E < n - 120 ? 0.0f : pow2i(E - n);
+        own |= plain;
         E = n;
+        if (own) df = pow2i(E - own_scale);
     };
     uint32_t bad = 0;                              // blocks of the tile at hand without a page
 
@@ -296,10 +301,10 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             }
         km = __reduce_max_sync(0xffffffffu, km);
         vm = __reduce_max_sync(0xffffffffu, vm);
-        if (max(km, vm) >= 0x7f80u) return true;
-        ek = max(static_cast<int>(km >> 7) - 127, -100);
-        raise_E(max(static_cast<int>(vm >> 7) - 127, -100));
-        return false;
+        const bool plain = max(km, vm) >= 0x7f80u;
+        if (!plain) ek = max(static_cast<int>(km >> 7) - 127, -100);
+        set_scale(max(static_cast<int>(vm >> 7) - 127, -100), plain);
+        return plain;
     };
     auto live_key = [&](int c) {
         return seen(unit_chunk(k, c) * kRtKeys + ku) && !((bad >> (ku >> 4)) & 1u);
@@ -414,9 +419,9 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
                     vm = max(vm, sm_mag[1][w]);
                 }
                 plain = max(km, vm) >= 0x7f800000u;
+                set_scale(static_cast<int>(vm >> 23) - 127, plain);
                 if (!plain) {
                     ek = max(ek, static_cast<int>(km >> 23) - 127);
-                    raise_E(static_cast<int>(vm >> 23) - 127);
                     load_f32(c, entry, a.k, x);
                     store_f32(sK, x, pow2i(10 - ek));
                 }
@@ -559,7 +564,9 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             // ---- plain loop over the tile ----
             const int ur = k.u0 + min(row, k.n_u - 1), h = hk * a.group + ur % a.group;
             const float* q = a.q + static_cast<long long>(s.row0 + ur / a.group) * a.q_ld + h * kHeadDim;
-            const float vs = pow2i(vbits - E);
+            const float vs = pow2i(vbits - own_scale);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= fac;
             for (int x = 0; x < kRtKeys; ++x) {
                 if (!((seen_bits(x >> 5) >> (x & 31)) & 1u)) continue;
                 const int j = j0 + x, p = page_entry(j), pr = j & pr_mask;
@@ -615,7 +622,8 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             umma_commit(&bar_o);
         }
         const bool running = !plain, more = c + 1 < c_end;
-        const float cf = corr * fac;               // (of this tile: preparing the next one may change fac)
+        const float cf = corr * fac, df_now = df;  // (of this tile: preparing the next one may change them)
+        const bool own_now = own;
         plain = more && prepare(c + 1, page1);
         if (running) {
             if (!mbar_wait_bounded(&bar_o, ph_o, nullptr)) s_fail = 1;
@@ -628,6 +636,10 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             for (int b = 0; b < 2; ++b) {
                 float d[16];
                 tmem_ld16(t_o + 16 * b, d);
+                if (own_now) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) d[i] *= df_now;
+                }
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                     float* x = o + 16 * b + i;
@@ -651,7 +663,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     if (row >= k.n_u) return;
     // a wait that gave up leaves the rows' sums NaN, their outputs 0
     const float L = s_fail ? __uint_as_float(0x7fc00000u) : l + sm_x[half ^ 1][row];
-    const float back = pow2i(E - vbits);
+    const float back = pow2i((own ? own_scale : E) - vbits);
     float y[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {

@@ -137,3 +137,43 @@ def test_a_first_tile_that_is_not_finite(kind, flat):
         if flat:
             s.k[0][n - 2, 0, 5] = 1.0
         _check(s, kv4)
+
+
+@pytest.mark.parametrize("value", [1e5, 1e9, 1e12, 1e30, 3e38])
+@pytest.mark.parametrize("what", ["k", "v", "kv"])
+@pytest.mark.parametrize("kind", [k for k in SHARED if k[0] and k[1] < 64 or not k[0] and k[1] < 3], ids=_id)
+def test_large_values_that_only_some_rows_see(kind, what, value):
+    kv4, r = kind
+    for n, window, at in ((r + 2, 0, -1), (400, 0, -1), (400, 100, 400 - r - 99)):
+        s = _stream(kind, n)
+        if "k" in what:
+            s.k[0][at, 0, 2] = value
+        if "v" in what:
+            s.v[0][at, 0, 2] = value
+        sees = np.arange(n - r, n) >= n - 1 if at < 0 else np.arange(n - r, n) - window < at
+        out = s.attend(kv4, window, 0, _caches(s, kv4))
+        s.torch.cuda.synchronize()
+        ref, tol = _reference(s, kv4, window, 0)
+        assert 0 < sees.sum() < r
+        check(out.cpu().numpy()[~sees], ref[~sees], tol[~sees], (n, window))
+        if "k" not in what:
+            check(out.cpu().numpy()[sees], ref[sees], tol[sees], (n, window))
+
+
+@pytest.mark.parametrize("value", [1e5, 1e9, 1e12, 1e30, 1e38])
+@pytest.mark.parametrize("kind", [k for k in KINDS if k[0] and k[1] < 64 or not k[0] and k[1] < 3], ids=_id)
+def test_large_values_without_weight(kind, value):
+    """A key far below the others' scores holds a large V: the outputs are the others'. The same for a large K."""
+    kv4, r = kind
+    for n, at in ((r + 30, 5), (700, 340)):
+        for large_k in (False, True):
+            s = _stream(kind, n)
+            s.q = (s.q[:1] * np.ones((r, 1, 1)) + 0.1 * s.q).astype(np.float32)
+            low = -s.q[0, 0] * np.float32(200)
+            s.k[0][at, 0] = np.where(np.abs(low) > 20, low, 0)
+            if large_k:
+                i = int(np.argmax(np.abs(s.q[0, 0])))
+                s.k[0][at, 0, i] = -np.sign(s.q[0, 0, i]) * value
+            else:
+                s.v[0][at, 0, 7] = value
+            _check(s, kv4)

@@ -23,6 +23,11 @@
 //                 accumulators that are added to the running f32 sums by ordinary fma, so that the
 //                 tensor cores' truncation does not build up over a long cache.
 //
+// E is shared by rows that see different keys, and f16 holds scales from 2^E down to 2^(E - 24) exactly. A
+// warp that met scales further apart throws its sums away and takes its keys again in a plain f32 loop,
+// several times as long; ordinary caches hold none (looking for them in every chunk, to leave only that chunk
+// to a plain loop, took 2 % of every call).
+//
 // With up to 4 unit rows (PAIR) columns 2 r and 2 r + 1 are row r's high and low parts: half the
 // products and half the softmax of the general form, where both parts take a product of their own.
 //
@@ -45,6 +50,7 @@ constexpr int kFewChunk = 64;
 constexpr int kFewWarps = 4;
 constexpr int kFewStages = 2;
 constexpr int kFewStageBytes = kFewChunk * 2 * kKv4RowBytes;   // K codes, V codes, K scales, V scales
+constexpr int kFewSpan = 24;             // scales from 2^E down to 2^(E - 24) are exact
 constexpr int kFewK = 0, kFewV = kFewChunk * 32, kFewKs = 2 * kFewChunk * 32, kFewVs = kFewKs + kFewChunk * 4;
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -257,6 +263,7 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
     auto row_of = [&](int nt, int b) { return PAIR ? t : nt * 8 + 2 * t + b; };
     float m[NT][NB], rf[NT][NB], l[NT][NB], o[NT][4][4];     // maximum, reference of the weights, sum, values
     int E = -100;                          // V is held times 2^(9 - E)
+    uint32_t low = 0xffffffffu;            // the lane's smallest V scales that are not 0, less 1, by group
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -328,6 +335,7 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
                                       (j >= seen_lo || j < a.sinks);
                     vw[w] = seen ? vw[w] : 0u;
                 }
+                low = __vminu2(low, vw[w] - 0x00010001u);          // (a zero gives 0xfffe or more)
                 z[w][0] = __uint_as_float(vw[w] << 16);
                 z[w][1] = __uint_as_float(vw[w] & 0xffff0000u);
                 big = fmaxf(big, fmaxf(fabsf(z[w][0]), fabsf(z[w][1])));
@@ -546,9 +554,69 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
     cp_async_wait<0>();
     __syncthreads();
 
-    // ---- join the warps: O as [unit row][dim], each warp's sums scaled back by 2^(E - 9) ----
+    float back = __uint_as_float(static_cast<uint32_t>(127 + E - 9) << 23);
+    if (__any_sync(0xffffffffu, static_cast<int>(min(low & 0xffffu, low >> 16)) + 1 < (127 + E - kFewSpan) << 7)) {
+        // ---- plain loop: thread = a word of 8 dims, the rows of its quad lane ----
+        float q[NT][NB][8];
+        back = 1.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int ur = k.u0 + min(row_of(nt, b), k.n_u - 1), h = hk * a.group + ur % a.group;
+                const float* src = a.q + static_cast<long long>(s.row0 + ur / a.group) * a.q_ld + h * kHeadDim + 8 * g;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) q[nt][b][n] = src[n];
+                rf[nt][b] = -INFINITY;
+                l[nt][b] = 0.0f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[nt][mt][j] = 0.0f;
+        }
+        for (int c = c0; c < c_end; c += kFewWarps)
+            for (int x = 0; x < kFewChunk; ++x) {
+                const int j = unit_chunk(k, c) * kFewChunk + x;
+                if (j >= end) break;
+                const int page = tab ? tab[j >> a.v.shift] : s.slot * a.v.pages_per_slot + (j >> a.v.shift);
+                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.v.n_pages)) continue;
+                const unsigned char* blk = base + static_cast<unsigned long long>(static_cast<unsigned>(page)) * page_bytes;
+                const int r = j & pr_mask, at = a.v.page_rows * 32 + r * 4 + (g >> 2) * 2;
+                const uint32_t kc = *reinterpret_cast<const uint32_t*>(blk + r * 32 + ((g & 3) * 2 + (g >> 2)) * 4);
+                uint32_t vc = *reinterpret_cast<const uint32_t*>(blk + part + r * 32 + g * 4);
+                vc = ((vc >> 2) & 0x3fff3fffu) | ((vc << 14) & 0xc000c000u);
+                const float ks = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(blk + at)) << 16);
+                const float vs = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(blk + part + at)) << 16);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        float sc = 0.0f;
+#pragma unroll
+                        for (int n = 0; n < 8; ++n)
+                            sc = fmaf(ks * static_cast<float>(static_cast<int>((kc >> (4 * n)) & 15u) - 8), q[nt][b][n], sc);
+                        sc += __shfl_xor_sync(0xffffffffu, sc, 4);
+                        sc += __shfl_xor_sync(0xffffffffu, sc, 8);
+                        sc = (sc + __shfl_xor_sync(0xffffffffu, sc, 16)) * (0.125f * kLog2e);
+                        const long long p = s.pos0 + (k.u0 + row_of(nt, b)) / a.group;
+                        if (!(j <= p && (a.window == 0 || j > p - a.window || j < a.sinks))) sc = -INFINITY;
+                        const float mn = fmaxf(rf[nt][b], sc), ref = mn == -INFINITY ? 0.0f : mn;
+                        const float cr = ex2(rf[nt][b] - ref), w = ex2(sc - ref);
+                        rf[nt][b] = mn;
+                        l[nt][b] = fmaf(l[nt][b], cr, g == 0 ? w : 0.0f);
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {
+                            float& on = o[nt][n >> 1][(n & 1) * 2 + b];
+                            on *= cr;
+                            if (w != 0.0f) on = fmaf(w, vs * static_cast<float>(static_cast<int>((vc >> (4 * n)) & 15u) - 8), on);
+                        }
+                    }
+            }
+    }
+
+    // ---- join the warps: O as [unit row][dim], each warp's sums scaled back ----
     float* so = reinterpret_cast<float*>(few_smem) + warp * UR * (kHeadDim + 4);
-    const float back = __uint_as_float(static_cast<uint32_t>(127 + E - 9) << 23);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

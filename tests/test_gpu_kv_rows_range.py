@@ -177,3 +177,14 @@ def test_large_values_without_weight(kind, value):
             else:
                 s.v[0][at, 0, 7] = value
             _check(s, kv4)
+
+
+@pytest.mark.parametrize("value", [1e30, 1e36, 3e-30])
+@pytest.mark.parametrize("n", [300, 4000])
+@pytest.mark.parametrize("kind", KINDS, ids=_id)
+def test_values_near_the_ends_of_the_range(kind, n, value):
+    """Sums over many keys of about equal weight: every one of them is a number in f32."""
+    s = _stream(kind, n)
+    s.q *= np.float32(0.01)
+    s.v[0] *= np.float32(value)
+    _check(s, kind[0])

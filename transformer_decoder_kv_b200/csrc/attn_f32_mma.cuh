@@ -356,14 +356,15 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const Ro
             sum += __shfl_xor_sync(0xffffffffu, sum, 8);
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
             const int u = nt * 8 + 2 * t + b;
+            const RowScale f = row_scale(m[nt][b], rf[nt][b]);
             if (g == 0) {
-                sm_m[warp][u] = rf[nt][b];
-                sm_l[warp][u] = sum;
+                sm_m[warp][u] = f.ref;
+                sm_l[warp][u] = sum * f.mul;
             }
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
                 *reinterpret_cast<float2*>(&sm_o[warp][u][8 * g + 2 * mt]) =
-                    make_float2(o[nt][mt][b] * back, o[nt][mt][b + 2] * back);
+                    make_float2(o[nt][mt][b] * (back * f.mul), o[nt][mt][b + 2] * (back * f.mul));
         }
     __syncthreads();
     for (int x = tid; x < k.n_u * 16; x += kF32Warps * 32) {

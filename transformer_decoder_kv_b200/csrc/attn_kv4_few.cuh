@@ -568,6 +568,7 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
 #pragma unroll
                 for (int n = 0; n < 8; ++n) q[nt][b][n] = src[n];
                 rf[nt][b] = -INFINITY;
+                m[nt][b] = INFINITY;               // (weights of at most 1)
                 l[nt][b] = 0.0f;
             }
 #pragma unroll
@@ -626,16 +627,17 @@ static __global__ void __launch_bounds__(kFewWarps * 32) k_attn_kv4_few(const Ro
             sum += __shfl_xor_sync(0xffffffffu, sum, 8);
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
             const int u = row_of(nt, b);
+            const RowScale f = row_scale(m[nt][b], rf[nt][b]);
             if (g == 0) {
-                sm_m[warp][u] = rf[nt][b];
-                sm_l[warp][u] = sum;
+                sm_m[warp][u] = f.ref;
+                sm_l[warp][u] = sum * f.mul;
             }
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
                 const float x = PAIR ? o[nt][mt][0] + o[nt][mt][1] : o[nt][mt][b];
                 const float y = PAIR ? o[nt][mt][2] + o[nt][mt][3] : o[nt][mt][b + 2];
                 *reinterpret_cast<float2*>(so + u * (kHeadDim + 4) + 8 * g + 2 * mt) =
-                    make_float2(x * back, y * back);
+                    make_float2(x * (back * f.mul), y * (back * f.mul));
             }
         }
     __syncthreads();

@@ -87,6 +87,16 @@ __host__ __device__ __forceinline__ int split_begin(const UnitKeys& k, int sp) {
     return static_cast<int>(static_cast<long long>(k.total) * sp / k.splits);
 }
 
+// The kernels on tensor cores weigh a key by 2^(s - ref) with ref 12 below the running maximum m (at it from 2^16
+// on): for the joins and the output the sums go to weights of at most 1, where they are finite as long as
+// f32 holds them at all. (ref + 12 is exact: a multiple of ref's last bit below 2^16.)
+struct RowScale {
+    float ref, mul;
+};
+__device__ __forceinline__ RowScale row_scale(float m, float ref) {
+    return fabsf(m) < 65536.0f ? RowScale{ref + 12.0f, 1.0f / 4096.0f} : RowScale{ref, 1.0f};
+}
+
 // A block's result of unit row u, dims 4 d4 .. 4 d4 + 3: the output, or this split's partial state.
 __device__ __forceinline__ void store_unit_row(const RowsAttnArgs& a, const UnitKeys& k, const StreamRows& s, int hk,
                                                int sp, int u, int d4, float m, float l, float4 o) {

@@ -662,8 +662,9 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     if (warp == 0) tmem_dealloc(tmem, kRtTmemCols);
     if (row >= k.n_u) return;
     // a wait that gave up leaves the rows' sums NaN, their outputs 0
-    const float L = s_fail ? __uint_as_float(0x7fc00000u) : l + sm_x[half ^ 1][row];
-    const float back = pow2i((own ? own_scale : E) - vbits);
+    const RowScale f = row_scale(m, ref_old);
+    const float L = s_fail ? __uint_as_float(0x7fc00000u) : (l + sm_x[half ^ 1][row]) * f.mul;
+    const float back = pow2i((own ? own_scale : E) - vbits) * f.mul;
     float y[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
@@ -672,7 +673,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        store_unit_row(a, k, s, hk, sp, row, half * 8 + i, ref_old, L,
+        store_unit_row(a, k, s, hk, sp, row, half * 8 + i, f.ref, L,
                        make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]));
 }
 

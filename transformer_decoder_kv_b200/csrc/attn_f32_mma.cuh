@@ -14,10 +14,12 @@
 // a key's four dims of one 16-dim step (K), or half of its 8 dims (V); V's pairs along the keys come from
 // the conversion of two keys' values at once.
 //
-// The powers of two of K and V stand while the values stay within f16's range; a chunk beyond them (the
-// first one, to begin with) sets them anew. A chunk that holds a NaN or an infinity is computed by a plain
-// f32 loop: in a matrix product it would reach rows that do not see it. From such a chunk on the sums are
-// kept in a scale of their own, 2^-16, in which f32 holds those of all finite values.
+// The powers of two of K and V stand while every key's largest value stays between 2^-2 and f16's end, where
+// 22 bits are left of it; a chunk outside (the first one, to begin with, and one with keys that no row sees)
+// is looked at more closely and may set them anew. A chunk whose keys lie 2^12 apart, or that holds a NaN or
+// an infinity, is computed by a plain f32 loop: a matrix product would take it to rows that do not see it. From
+// a plain chunk on, or from one that needs a smaller power of two than those before, the sums are kept in a
+// scale of their own, 2^-16, in which f32 holds those of all finite values.
 #pragma once
 
 #include "attn_f32_few.cuh"
@@ -26,6 +28,7 @@
 namespace dec {
 
 constexpr int kMmaOwnScale = 26;           // o is held times 2^(10 - 26)
+constexpr int kMmaSpan = 12;               // keys' largest values from 2^e down to 2^(e - 12)
 
 template <int NT>
 static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const RowsAttnArgs a) {
@@ -148,11 +151,6 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const Ro
         lo = h2_bits(__floats2half2_rn(v.x - f.x, v.y - f.y));
         big = __hmax2_nan(big, __habs2(h));
     };
-    auto off_range = [](__half2 big) {             // an infinity or a NaN
-        const uint32_t x = h2_bits(big);
-        return (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u;
-    };
-
     for (; c < c_end; c += kF32Warps) {
         const int j0 = unit_chunk(k, c) * kF32Chunk;
         const bool full = at >= 0 && j0 <= full_hi && j0 + kF32Chunk <= end && (j0 >= full_lo || j0 + kF32Chunk <= a.sinks);
@@ -176,46 +174,75 @@ static __global__ void __launch_bounds__(kF32Warps * 32) k_attn_f32_mma(const Ro
         bool plain = false;
         auto convert = [&]() {
             const float ku = pow2(10 - ek), vu = pow2(10 - E);
-            __half2 big = __float2half2_rn(0.0f);
+            const __half2 zero = __float2half2_rn(0.0f);
+            __half2 bk[2] = {zero, zero}, bv[2] = {zero, zero};          // largest halves by key
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    halves(kk[h][ks].x, kk[h][ks].y, ku, kh[ks][h], kl[ks][h], big);
-                    halves(kk[h][ks].z, kk[h][ks].w, ku, kh[ks][2 + h], kl[ks][2 + h], big);
+                    halves(kk[h][ks].x, kk[h][ks].y, ku, kh[ks][h], kl[ks][h], bk[h]);
+                    halves(kk[h][ks].z, kk[h][ks].w, ku, kh[ks][2 + h], kl[ks][2 + h], bk[h]);
                 }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {      // keys 2 t, 2 t + 1, then + 8
                     const float4 x = vv[2 * i][h], y = vv[2 * i + 1][h];
-                    halves(x.x, y.x, vu, vh[2 * h][2 * i], vl[2 * h][2 * i], big);
-                    halves(x.y, y.y, vu, vh[2 * h][2 * i + 1], vl[2 * h][2 * i + 1], big);
-                    halves(x.z, y.z, vu, vh[2 * h + 1][2 * i], vl[2 * h + 1][2 * i], big);
-                    halves(x.w, y.w, vu, vh[2 * h + 1][2 * i + 1], vl[2 * h + 1][2 * i + 1], big);
+                    halves(x.x, y.x, vu, vh[2 * h][2 * i], vl[2 * h][2 * i], bv[i]);
+                    halves(x.y, y.y, vu, vh[2 * h][2 * i + 1], vl[2 * h][2 * i + 1], bv[i]);
+                    halves(x.z, y.z, vu, vh[2 * h + 1][2 * i], vl[2 * h + 1][2 * i], bv[i]);
+                    halves(x.w, y.w, vu, vh[2 * h + 1][2 * i + 1], vl[2 * h + 1][2 * i + 1], bv[i]);
                 }
-            return __any_sync(0xffffffffu, off_range(big));
+            // (of the lane's part of each key: a smaller part is looked at, too; a NaN fails the first test)
+            const __half2 big = __hmax2_nan(__hmax2_nan(bk[0], bk[1]), __hmax2_nan(bv[0], bv[1]));
+            const __half2 low = __hmin2(__hmin2(bk[0], bk[1]), __hmin2(bv[0], bv[1]));
+            const bool fits = __hblt2(big, bits_h2(0x7c007c00u)) && __hbge2(low, bits_h2(0x34003400u));
+            return __any_sync(0xffffffffu, !fits);
         };
         if (convert()) {
-            uint32_t km = 0, vm = 0;
+            // each key's largest magnitude, as bits (a NaN's are above all); the smallest of those above 0, less 1
+            uint32_t top[2], least[2];             // K, V
             auto mag = [](const float4& x) {
                 return max(max(__float_as_uint(fabsf(x.x)), __float_as_uint(fabsf(x.y))),
                            max(__float_as_uint(fabsf(x.z)), __float_as_uint(fabsf(x.w))));
             };
+            top[0] = top[1] = 0u;
+            least[0] = least[1] = 0xffffffffu;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                km = max(km, mag(kk[i >> 2][i & 3]));
-                vm = max(vm, mag(vv[i >> 1][i & 1]));
+            for (int i = 0; i < 6; ++i) {
+                uint32_t x;
+                if (i < 2) {
+                    x = max(max(mag(kk[i][0]), mag(kk[i][1])), max(mag(kk[i][2]), mag(kk[i][3])));
+                    x = max(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = max(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                } else {
+                    x = max(mag(vv[i - 2][0]), mag(vv[i - 2][1]));
+                    x = max(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = max(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = max(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                }
+                top[i >= 2] = max(top[i >= 2], x);
+                least[i >= 2] = min(least[i >= 2], x - 1u);
             }
-            km = __reduce_max_sync(0xffffffffu, km);
-            vm = __reduce_max_sync(0xffffffffu, vm);
-            plain = max(km, vm) >= 0x7f800000u;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+                least[i] = __reduce_min_sync(0xffffffffu, least[i]);
+                const int t2 = static_cast<int>(top[i] & 0x7f800000u) - (kMmaSpan << 23);
+                plain |= top[i] >= 0x7f800000u || (t2 > 0 && least[i] < static_cast<uint32_t>(t2) - 1u);
+            }
             if (!plain) {
-                ek = max(ek, static_cast<int>(km >> 23) - 127);
-                const int e = max(E, static_cast<int>(vm >> 23) - 127);
-                if (!own) fac = E < e - 120 ? 0.0f : pow2(E - e);
-                E = e;
+                if (top[0]) ek = max(static_cast<int>(top[0] >> 23) - 127, -100);
                 kscale = pow2(ek - 10);
+                const int e = max(static_cast<int>(top[1] >> 23) - 127, -100);
+                if (!own && top[1]) {
+                    // smaller than the sums' scale leaves bits for, or far from 1: the sums' own scale
+                    own = e > 40 || e < -40 || static_cast<int>(least[1] >> 23) - 127 < E - kMmaSpan;
+                    const int to = own ? kMmaOwnScale : max(E, e);
+                    fac = E < to - 120 ? 0.0f : pow2(E - to);              // (E is -100 before any value)
+                    E = max(E, e);
+                }
+                if (own && top[1]) E = e;
                 convert();
             }
         }

@@ -23,9 +23,12 @@
 // rows over 4096 keys, 14 heads over 2: 163 us, 182 TFLOP/s counted once (f32: 102); a warp of its own for
 // the issue, a queue of work on the device and 96 registers for more warps were all slower.
 //
-// A tile that holds a NaN or an infinity in K or V, at a position that some row sees, is computed by a
-// plain f32 loop instead: in a matrix product it would reach the rows that do not see it. From such a tile
-// on the sums are kept in a scale of their own, 2^-16, in which f32 holds those of all finite values.
+// All rows share a tile's powers of two, also for keys that only some of them see. Of a 4-bit cache f16 holds
+// scales down to 2^-24 of the tile's largest exactly, of an f32 cache 22 bits of every key's largest value down
+// to 2^-12 of the tile's. A tile with keys further apart, or with a NaN or an infinity at a position that some
+// row sees, is computed by a plain f32 loop instead. From a plain tile on, or from one that needs a smaller
+// power of two of V than those before, the sums are kept in a scale of their own, 2^-16, in which f32 holds
+// those of all finite values.
 #pragma once
 
 #include "attn_kv4_few.cuh"
@@ -38,6 +41,7 @@ constexpr int kRtPlane = kRtRows * 128;           // one f16 operand plane: 128 
 constexpr uint32_t kRtTmemCols = 256;             // S / P 0..127, O 128..191
 // a tile of a 4-bit cache as it lies: K codes, V codes, K scales, V scales
 constexpr int kRtStage = kRtKeys * 2 * kKv4RowBytes;
+constexpr int kRtSpan4 = 24, kRtSpan = 12;        // scales, and keys' largest values: from 2^e down to 2^(e - span)
 constexpr int kRtV = kRtKeys * 32, kRtKs = 2 * kRtKeys * 32, kRtVs = kRtKs + kRtKeys * 4;
 template <bool KV4>
 constexpr int rt_smem_bytes() {
@@ -152,7 +156,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     __shared__ uint32_t s_tmem;
     __shared__ float sm_f[kRtRows], sm_x[2][kRtRows];            // row factors; column halves' maxima, sums
     __shared__ uint32_t sm_bad[2][8];                            // of a tile's 16-key blocks: no page
-    __shared__ uint32_t sm_mag[2][8];                            // f32: magnitudes of K, of V
+    __shared__ uint32_t sm_mag[4][8];                            // f32: magnitudes of K, of V; the smallest
     __shared__ int s_fail;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -272,11 +276,15 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     int ek = -100, E = -100;                       // K is held times 2^(10 - ek), V times 2^(vbits - E)
     bool own = false;                              // O is held times 2^-16, or else as V
     float fac = 1.0f, df = 1.0f;                   // what the last change of scale makes of O, and P V's scale
-    auto set_scale = [&](int e, bool plain) {
-        const int n = plain ? E : max(E, e);
-        if (!own) fac = plain ? pow2i(E - own_scale) : E < n - 120 ? 0.0f : pow2i(E - n);
-        own |= plain;
-        E = n;
+    // For a tile whose V has the largest exponent e; `small`: some key is too small for the scale so far.
+    auto set_scale = [&](int e, bool small, bool plain) {
+        if (!own) {
+            own = plain || e > 40 || e < -40 || small;
+            const int to = own ? own_scale : max(E, e);
+            fac = E < to - 120 ? 0.0f : pow2i(E - to);         // (E is -100 before any value)
+            if (!plain) E = max(E, e);
+        }
+        if (own && !plain) E = min(max(e, -100), 123);
         if (own) df = pow2i(E - own_scale);
     };
     uint32_t bad = 0;                              // blocks of the tile at hand without a page
@@ -292,18 +300,24 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
         const unsigned char* st = stages + buf * kRtStage + lane * 16;
         const uint4 kv = *reinterpret_cast<const uint4*>(st + kRtKs), vv = *reinterpret_cast<const uint4*>(st + kRtVs);
         const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, vw[4] = {vv.x, vv.y, vv.z, vv.w};
-        uint32_t km = 0, vm = 0;
+        uint32_t km = 0, vm = 0, kl = 0xffffffffu, vl = 0xffffffffu;     // largest; smallest above 0, less 1, by group
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (live || (seen(j0 + lane * 4 + i) && !((bad >> (lane >> 2)) & 1u))) {
-                km = max(km, max(kw[i] & 0xffffu, kw[i] >> 16));
-                vm = max(vm, max(vw[i] & 0xffffu, vw[i] >> 16));
+                km = __vmaxu2(km, kw[i]);
+                vm = __vmaxu2(vm, vw[i]);
+                kl = __vminu2(kl, kw[i] - 0x00010001u);            // (a zero gives 0xfffe or more)
+                vl = __vminu2(vl, vw[i] - 0x00010001u);
             }
-        km = __reduce_max_sync(0xffffffffu, km);
-        vm = __reduce_max_sync(0xffffffffu, vm);
-        const bool plain = max(km, vm) >= 0x7f80u;
-        if (!plain) ek = max(static_cast<int>(km >> 7) - 127, -100);
-        set_scale(max(static_cast<int>(vm >> 7) - 127, -100), plain);
+        km = __reduce_max_sync(0xffffffffu, max(km & 0xffffu, km >> 16));
+        vm = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16));
+        const int ke = static_cast<int>(km >> 7) - 127, e = static_cast<int>(vm >> 7) - 127;
+        const int kleast = static_cast<int>((min(kl & 0xffffu, kl >> 16) + 1u) >> 7) - 127;
+        const int least = static_cast<int>((min(vl & 0xffffu, vl >> 16) + 1u) >> 7) - 127;
+        bool plain = max(km, vm) >= 0x7f80u;
+        plain |= __any_sync(0xffffffffu, kleast < ke - kRtSpan4 || least < e - kRtSpan4);
+        if (!plain) ek = max(ke, -100);
+        if (plain || vm) set_scale(e, __any_sync(0xffffffffu, least < E - kRtSpan4), plain);
         return plain;
     };
     auto live_key = [&](int c) {
@@ -397,31 +411,42 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
             __syncthreads();
         } else {
             // The powers of two stand while the values, held below 2^11 when they were set, stay below 2^15
-            // (2^16 itself would not do: f16 ends at 65504); a tile beyond them (the first one, to begin
-            // with) sets them anew.
+            // (2^16 itself would not do: f16 ends at 65504) and every key's largest at 2^-2 or more; a tile
+            // beyond them (the first one, to begin with) sets them anew.
             float4 x[8];
             load_f32(c, entry, a.k, x);
             uint32_t km = magnitude(x);
             store_f32(sK, x, pow2i(10 - ek));
             load_f32(c, entry, a.vv, vf);
             uint32_t vm = magnitude(vf);
-            const uint32_t klim = static_cast<uint32_t>(min(127 + ek + 5, 255)) << 23;
-            const uint32_t vlim = static_cast<uint32_t>(min(127 + E + 5, 255)) << 23;
+            // (of half a key: a smaller half is looked at, too)
+            const uint32_t klow = static_cast<uint32_t>(127 + ek - kRtSpan) << 23;
+            const uint32_t vlow = static_cast<uint32_t>(127 + E - kRtSpan) << 23;
+            constexpr uint32_t range = (kRtSpan + 5) << 23;
             fence_async_smem();
-            if (__syncthreads_or(c == c0 || km >= klim || vm >= vlim)) {
+            if (__syncthreads_or(c == c0 || (km && km - klow >= range) || (vm && vm - vlow >= range))) {
+                km = max(km, __shfl_xor_sync(0xffffffffu, km, 1));
+                vm = max(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+                // largest of all keys, smallest above 0 less 1
+                const uint32_t kl = __reduce_min_sync(0xffffffffu, km - 1u), vl = __reduce_min_sync(0xffffffffu, vm - 1u);
                 km = __reduce_max_sync(0xffffffffu, km);
                 vm = __reduce_max_sync(0xffffffffu, vm);
-                if (lane == 0) sm_mag[0][warp] = km, sm_mag[1][warp] = vm;
+                if (lane == 0) sm_mag[0][warp] = km, sm_mag[1][warp] = vm, sm_mag[2][warp] = kl, sm_mag[3][warp] = vl;
                 __syncthreads();
+                uint32_t kleast = kl, least = vl;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) {
                     km = max(km, sm_mag[0][w]);
                     vm = max(vm, sm_mag[1][w]);
+                    kleast = min(kleast, sm_mag[2][w]);
+                    least = min(least, sm_mag[3][w]);
                 }
-                plain = max(km, vm) >= 0x7f800000u;
-                set_scale(static_cast<int>(vm >> 23) - 127, plain);
+                const int ke = static_cast<int>(km >> 23) - 127, e = static_cast<int>(vm >> 23) - 127;
+                const int kmin = static_cast<int>(kleast >> 23) - 127, vmin = static_cast<int>(least >> 23) - 127;
+                plain = max(km, vm) >= 0x7f800000u || kmin < ke - kRtSpan || vmin < e - kRtSpan;
+                if (plain || vm) set_scale(e, vmin < E - kRtSpan, plain);
                 if (!plain) {
-                    ek = max(ek, static_cast<int>(km >> 23) - 127);
+                    if (km) ek = min(max(ke, -100), 123);
                     load_f32(c, entry, a.k, x);
                     store_f32(sK, x, pow2i(10 - ek));
                 }

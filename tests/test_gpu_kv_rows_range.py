@@ -188,3 +188,21 @@ def test_values_near_the_ends_of_the_range(kind, n, value):
     s.q *= np.float32(0.01)
     s.v[0] *= np.float32(value)
     _check(s, kind[0])
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=_id)
+def test_the_low_halves_of_operands_count(kind):
+    """Three keys with scores of 1 and -1, one operand 2^-12 off its nearest f16 in every element. Left at 11
+    bits it takes a score 2^-12 off and the output 2^-14 (weights 0.79 and 0.21), or a value 2^-12 off; the
+    tolerance is 2^-16 and less. (Equal scores: the weights' own bits.)"""
+    kv4, r = kind
+    off = np.float32(1 + 2.0 ** -11 + 2.0 ** -12)         # f16 has 1 and 1 + 2^-10
+    sign = np.where(np.arange(D) % 2, 1, -1).astype(np.float32)
+    for q, k, v in ((off, 1, 1), (1, off, 1), (0.01, 1, off), (0.01, 1, 1)):
+        s = _stream(kind, max(3, r), page_rows=64)
+        s.q[:, 0] = sign * np.float32(0.25) * np.float32(q)
+        s.k[0][:, 0] = sign * np.float32(0.5)
+        s.k[0][::2, 0] *= -np.float32(k)
+        s.v[0][:, 0] = np.float32(v)
+        s.v[0][::2, 0] = np.float32(-1 - 2.0 ** -5)
+        _check(s, kv4)

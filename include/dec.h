@@ -506,8 +506,8 @@ dec_status dec_i8_dot(const int8_t* xq, const int8_t* wq, int32_t m, int32_t n, 
  *              outside [0, n_slots) has no rows.
  *   lens       device int32 [batch]. Positions below 0 or beyond the slot's rows are not
  *              stored and read back as zeros; a query below position 0 gives zeros.
- * The structs are host memory, read during the call; the device arrays are read by the queued
- * kernels. The calls need no handle, allocate nothing, run on the calling thread's current
+ * The structs are host memory, read during the call; the device arrays (4-byte aligned) are read
+ * by the queued kernels. The calls need no handle, allocate nothing, run on the calling thread's current
  * device, do not synchronise, and can be captured into CUDA graphs (make a first call on the
  * device before: it may load the module); a replay reads the device arrays anew. Errors set
  * dec_last_error(NULL).

@@ -1,0 +1,29 @@
+"""More of what the row-batch operators refuse, on the host before any CUDA call (CPU only)."""
+import ctypes as C
+
+import pytest
+
+from transformer_decoder_kv_b200 import binding as b
+
+P = 1 << 20      # an aligned address; a refused call never reads it
+
+
+def _calls(table=None, row_start=P, slots=None, lens=P):
+    lib = b.lib()
+    view, rows = b.DecKvView(2, 16, 4, 3, 12, table), b.DecKvRows(3, 10, 5, row_start, slots, lens)
+    v, r = C.byref(view), C.byref(rows)
+    yield lib.dec_kv4_write(v, r, P, P, 128, P, None)
+    yield lib.dec_kv4_write_scaled(v, r, P, P, 128, P, 1, None)
+    yield lib.dec_kv4_read(v, r, P, P, P, 128, None)
+    yield lib.dec_attention_kv4(v, r, P, 256, 4, P, 0, 0, P, 256, P, 1 << 40, None)
+    yield lib.dec_attention_window(v, r, P, 256, 4, P, P, 0, 0, P, 256, P, 1 << 40, None)
+    assert lib.dec_attention_rows_workspace_size(v, r, 4) == 0
+
+
+@pytest.mark.parametrize("name", ["table", "row_start", "slots", "lens"])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_index_arrays_off_their_alignment(name, off):
+    for st in _calls(**{name: P + off}):
+        assert st == b.DEC_EINVAL
+        msg = b.lib().dec_last_error(None).decode()
+        assert name in msg and "4-byte" in msg

@@ -123,6 +123,8 @@ inline dec_status rows_cuda_fail(const char* who, cudaError_t e, const char* wha
     return rows_fail(who, DEC_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
 // Message of what is wrong with a view, or null. kv4: pages of 16, 32 or 64 rows only.
 inline const char* view_problem(const dec_kv_view* v, bool kv4) {
     if (!v) return "null view";
@@ -136,12 +138,15 @@ inline const char* view_problem(const dec_kv_view* v, bool kv4) {
     if (static_cast<long long>(v->n_slots) * v->pages_per_slot > 0x7fffffffll) return "too many logical pages";
     if (!v->table && static_cast<long long>(v->n_slots) * v->pages_per_slot > v->n_pages)
         return "without a table n_pages must hold n_slots * pages_per_slot pages";
+    if (!aligned4(v->table)) return "table must be 4-byte aligned";
     return nullptr;
 }
 
 inline const char* rows_problem(const dec_kv_rows* r) {
     if (!r) return "null rows";
     if (!r->lens) return "null lens";
+    if (!aligned4(r->row_start) || !aligned4(r->slots) || !aligned4(r->lens))
+        return "row_start, slots and lens must be 4-byte aligned";
     if (r->batch < 1 || r->batch > 65535) return "batch must be in [1, 65535]";
     if (r->n_rows < 1) return "n_rows must be >= 1";
     if (r->max_rows < 1 || r->max_rows > r->n_rows) return "max_rows must be in [1, n_rows]";

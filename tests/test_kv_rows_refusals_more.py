@@ -27,3 +27,11 @@ def test_index_arrays_off_their_alignment(name, off):
         assert st == b.DEC_EINVAL
         msg = b.lib().dec_last_error(None).decode()
         assert name in msg and "4-byte" in msg
+
+
+def test_a_workspace_of_negative_size():
+    import torch
+    rows = type("Rows", (), {"device": None})()
+    for n in (-1, -(1 << 40)):
+        with pytest.raises(b.DecError, match=f"needs {n}"):
+            b._scratch(rows, torch.zeros(4), n)

@@ -404,7 +404,7 @@ def _scratch(rows, workspace, workspace_bytes: int) -> Optional[int]:
     """Pointer of a workspace of at least workspace_bytes on the batch's device."""
     if not hasattr(workspace, "data_ptr"):
         _einval("workspace: must be a device tensor")
-    if workspace.nbytes < workspace_bytes or not workspace.is_contiguous():
+    if not 0 <= workspace_bytes <= workspace.nbytes or not workspace.is_contiguous():
         _einval(f"workspace: {workspace.nbytes} bytes (contiguous: {workspace.is_contiguous()}), needs {workspace_bytes}")
     if workspace.device != rows.device if rows.device is not None else not workspace.is_cuda:
         _einval(f"workspace: must be on {rows.device or 'a CUDA device'}, is on {workspace.device}")

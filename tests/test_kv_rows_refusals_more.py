@@ -35,3 +35,29 @@ def test_a_workspace_of_negative_size():
     for n in (-1, -(1 << 40)):
         with pytest.raises(b.DecError, match=f"needs {n}"):
             b._scratch(rows, torch.zeros(4), n)
+
+
+BIG = [1 << 31, 1 << 32, (1 << 32) + 1, -(1 << 31) - 1]
+
+
+@pytest.mark.parametrize("n", BIG)
+def test_whole_numbers_beyond_32_bits(n):
+    for i in range(5):
+        a = [2, 16, 4, 3, 12]
+        a[i] = n
+        with pytest.raises(b.DecError, match="beyond 32 bits"):
+            b.KvView(*a)
+    for kw in (dict(batch=n), dict(batch=1, n_rows=n), dict(batch=1, max_rows=n)):
+        with pytest.raises(b.DecError, match="beyond 32 bits"):
+            b.KvRows(lens=None, **kw)
+    view = b.KvView(2, 16, 4, 3)
+    rows = type("Rows", (), {"torch": None, "ref": None})()
+    with pytest.raises(b.DecError, match="beyond 32 bits"):
+        b.attention_rows_workspace_size(view, rows, n)
+    for kw in (dict(window=n), dict(sinks=n)):
+        with pytest.raises(b.DecError, match="beyond 32 bits"):
+            b.attention_kv4(view, rows, None, None, 4, None, None, 0, **kw)
+        with pytest.raises(b.DecError, match="beyond 32 bits"):
+            b.attention_window(view, rows, None, None, None, 4, None, None, 0, **kw)
+    with pytest.raises(b.DecError, match="beyond 32 bits"):
+        b.attention_kv4(view, rows, None, None, n, None, None, 0)

@@ -383,6 +383,13 @@ def _einval(msg: str):
     raise DecError(DEC_EINVAL, msg)
 
 
+def _int32(**values):
+    """Whole numbers that the C structs and calls hold in 32 bits (ctypes would cut them)."""
+    for name, v in values.items():
+        if not -0x80000000 <= v <= 0x7fffffff:
+            _einval(f"{name}: {v} is beyond 32 bits")
+
+
 def _device_array(name: str, a, dtype: str, least: int, device=None) -> Optional[int]:
     """Pointer of a contiguous device array of at least `least` elements of a type."""
     if a is None:
@@ -452,6 +459,8 @@ class KvView:
 
     def __init__(self, n_kv_heads: int, page_rows: int, pages_per_slot: int, n_slots: int, n_pages: int = 0,
                  table=None):
+        _int32(n_kv_heads=n_kv_heads, page_rows=page_rows, pages_per_slot=pages_per_slot, n_slots=n_slots,
+               n_pages=n_pages or n_slots * pages_per_slot)
         self.table = table          # kept alive with the description
         self.device = getattr(table, "device", None)
         ptr = _device_array("table", table, "int32", n_slots * pages_per_slot)
@@ -467,6 +476,7 @@ class KvRows:
     and row_start are int32 device arrays; they may be rewritten between calls (or replays)."""
 
     def __init__(self, batch: int, lens, slots=None, row_start=None, n_rows: int = 0, max_rows: int = 1):
+        _int32(batch=batch, n_rows=n_rows, max_rows=max_rows)
         self.keep = (lens, slots, row_start)
         self.device = getattr(lens, "device", None)
         self.c = DecKvRows(batch, n_rows or batch, max_rows,
@@ -529,6 +539,7 @@ def _pool(view: KvView, rows: KvRows, cache) -> Optional[int]:
 
 def attention_rows_workspace_size(view: KvView, rows: KvRows, n_heads: int) -> int:
     """Scratch bytes of attention_kv4 / attention_window for these sizes."""
+    _int32(n_heads=n_heads)
     n = int(lib().dec_attention_rows_workspace_size(view.ref, rows.ref, n_heads))
     if n == 0:
         _einval("dec_attention_rows_workspace_size: bad view, rows or n_heads")
@@ -540,6 +551,8 @@ def attention_kv4(view: KvView, rows: KvRows, q, cache, n_heads: int, out, works
     """Attention of the batch's query rows (f32 [n_rows, n_heads * 64]) over a 4-bit cache: each sees
     the keys up to its own position, the last `window` of them (0: all) and the first `sinks`."""
     _same_device(view, rows)
+    if (window | sinks | n_heads) >> 31:
+        _int32(window=window, sinks=sinks, n_heads=n_heads)
     qp, q_ld = _rows_2d("q", q, rows, n_heads * 64)
     op, o_ld = _rows_2d("out", out, rows, n_heads * 64)
     _raise_thread_error(lib().dec_attention_kv4(view.ref, rows.ref, qp, q_ld, n_heads, _pool(view, rows, cache), window, sinks,
@@ -551,6 +564,8 @@ def attention_window(view: KvView, rows: KvRows, q, k, v, n_heads: int, out, wor
                      window: int = 0, sinks: int = 0, stream: int = 0):
     """attention_kv4 over f32 caches k and v ([n_pages, n_kv_heads, page_rows, 64] each)."""
     _same_device(view, rows)
+    if (window | sinks | n_heads) >> 31:
+        _int32(window=window, sinks=sinks, n_heads=n_heads)
     qp, q_ld = _rows_2d("q", q, rows, n_heads * 64)
     op, o_ld = _rows_2d("out", out, rows, n_heads * 64)
     least = view.c.n_pages * view.c.n_kv_heads * view.c.page_rows * 64

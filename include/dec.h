@@ -576,9 +576,17 @@ dec_status dec_kv4_read(const dec_kv_view* view, const dec_kv_rows* rows, const 
  * gives zeros, as in dec_attention (a query with an element of 2^112 or more may be taken as one,
  * and a bounded device wait that gives up, after about a second, leaves its rows zero). Values of
  * keys a query does not see never reach it, whatever they are (NaN, infinities, rows never
- * written). A row's result depends on its own stream and on the batch's shape (batch, max_rows,
- * n_heads, the view), which decides how its keys are split, not on the other streams' contents or
- * on when blocks run: equal calls give equal bits.
+ * written). A row's result depends on its own stream and on the call's shape (batch, n_rows, max_rows,
+ * n_heads, window, sinks, the view), which decides how its keys are split: other streams enter by the
+ * number of rows, padding rows included, but not by their contents, and neither does when blocks run.
+ * Equal calls give equal bits.
+ * Accuracy: sums are f32. One or two query rows per K/V head over f32 caches are computed in f32
+ * throughout. Elsewhere q, the weights and an f32 cache's k and v are pairs of f16 values: a score is
+ * within 2^-18 of sum |q_d k_d| / 8 and 2^-22 of (max |q_d| sum |k_d| + max |k_d| sum |q_d|) / 8, a
+ * weight within 2^-22 of itself and 2^-37 of the row's largest, a value within 2^-22 of its key's
+ * largest. Keys further apart than f16 pairs can hold (the largest values of two keys by 2^12 over
+ * f32 caches, two scales by 2^24 over 4-bit ones) are computed in plain f32, 10 to 100 times as long
+ * for the keys next to them.
  *   q, out    device f32 [n_rows] rows of n_heads * 64, q_ld and out_ld floats apart (multiples of 4)
  *   n_heads   a multiple of n_kv_heads
  *   workspace device scratch of dec_attention_rows_workspace_size(view, rows, n_heads) bytes. Its

@@ -1,9 +1,9 @@
 // Attention over f32 caches for units of one or two query rows (decoding tokens without grouped heads):
 // k_attn_f32_few<R>, up to R unit rows; attn_f32_mma.cuh takes more.
 //
-// Bound by the cache's 512 bytes per key: 64 streams x 4096 keys x 16 heads take 294 us, 7.3 TB/s. At HBM's
-// rate a key leaves an SM time for about 90 instructions, and on CUDA cores a key takes about 8 per unit
-// row, so nothing is staged and no product goes to the tensor cores: a warp loads
+// Bound by the cache's 512 bytes per key: 64 streams x 4096 keys x 16 heads take 327 us, 6.6 TB/s, and 256 x
+// 8192 x 2 303 us, 7.1 TB/s. At HBM's rate a key leaves an SM time for about 90 instructions, and on CUDA cores
+// a key takes about 8 per unit row, so nothing is staged and no product goes to the tensor cores: a warp loads
 // 16 keys of K and of V (a row per 16 lanes, 16 bytes a lane) straight into registers, 8 KB in flight
 // per warp, the next chunk's K while it works on V and the next V while it works on K.
 //

@@ -7,7 +7,7 @@
 // that loaded it, and tcgen05's tiles of 128 rows would stand nearly empty): K, V and Q are scaled by
 // powers of two and split into f16 high and low parts (22 bits), three products each, f32 sums;
 // the product of two low parts, below 2^-22, is left out. About 23 instructions per key; 256 streams x
-// 8192 keys x 2 heads take 401 us with 7 rows (5.4 TB/s; 689 on CUDA cores) and 491 with 16.
+// 8192 keys x 2 heads take 400 us with 7 rows (5.4 TB/s; 689 on CUDA cores) and 498 with 16.
 //
 // Fragments as in the 4-bit kernel: S^T = K Q^T with keys in the rows, softmax per column, P^T by movmatrix,
 // O^T += V^T P^T with 8 dims per quad lane and each chunk's sums in fresh accumulators. A 16-byte load is

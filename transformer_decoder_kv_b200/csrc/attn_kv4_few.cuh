@@ -24,9 +24,9 @@
 //                 tensor cores' truncation does not build up over a long cache.
 //
 // E is shared by rows that see different keys, and f16 holds scales from 2^E down to 2^(E - 24) exactly. A
-// warp that met scales further apart throws its sums away and takes its keys again in a plain f32 loop,
-// several times as long; ordinary caches hold none (looking for them in every chunk, to leave only that chunk
-// to a plain loop, took 2 % of every call).
+// warp that met scales further apart throws its sums away and takes its keys again in a plain f32 loop (64
+// streams x 4096 keys x 16 heads 1.4 ms where all warps do, instead of 78 us); ordinary caches hold none, and
+// looking for them in every chunk, to leave only that chunk to a plain loop, took 2 % of every call.
 //
 // With up to 4 unit rows (PAIR) columns 2 r and 2 r + 1 are row r's high and low parts: half the
 // products and half the softmax of the general form, where both parts take a product of their own.

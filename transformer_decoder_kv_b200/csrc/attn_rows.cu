@@ -1,5 +1,6 @@
 // dec_attention_kv4 and dec_attention_window: argument checks, the choice of kernel and split, and
-// the launches (kernels: attn_rows.cuh, attn_kv4_few.cuh).
+// the launches (kernels: attn_kv4_few.cuh, attn_f32_few.cuh, attn_f32_mma.cuh, attn_rows_tc.cuh; the
+// join of splits: attn_rows.cuh).
 #include <algorithm>
 
 #include "attn_f32_few.cuh"

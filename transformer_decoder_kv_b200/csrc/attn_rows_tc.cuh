@@ -17,16 +17,17 @@
 // that issues a product is held for as long as the product runs, so the warps share the rest: warp 0
 // issues P V while warps 4..7 unpack the next tile's K, then warp 4 issues Q K^T while warps 0..3 unpack
 // its V; the other block of the SM fills the gaps. A 4-bit cache's tile is copied into shared memory by
-// cp.async a tile ahead; an f32 tile goes through registers, half a key per thread. An M128 N128 K16 MMA takes 65 SM cycles and an M128 N64 K16 one 45 to 49
-// (measured), 1240 per tile of a 4-bit cache; the softmax, about 6 instructions per score and an exp2
-// unit that takes 1024 cycles per tile, is the larger part of a tile's time. 16 streams' chunks of 128
-// rows over 4096 keys, 14 heads over 2: 163 us, 182 TFLOP/s counted once (f32: 102); a warp of its own for
-// the issue, a queue of work on the device and 96 registers for more warps were all slower.
+// cp.async a tile ahead; an f32 tile goes through registers, half a key per thread. An M128 N128 K16 MMA
+// takes 65 SM cycles and an M128 N64 K16 one 45 to 49 (measured), 1240 per tile of a 4-bit cache; the
+// softmax, about 6 instructions per score and an exp2 unit that takes 1024 cycles per tile, is the larger
+// part of a tile's time. 16 streams' chunks of 128 rows over 4096 keys, 14 heads over 2: 156 us, 190 TFLOP/s
+// counted once (f32: 286 us, 104); a warp of its own for the issue, a queue of work on the device and 96
+// registers for more warps were all slower.
 //
 // All rows share a tile's powers of two, also for keys that only some of them see. Of a 4-bit cache f16 holds
 // scales down to 2^-24 of the tile's largest exactly, of an f32 cache 22 bits of every key's largest value down
 // to 2^-12 of the tile's. A tile with keys further apart, or with a NaN or an infinity at a position that some
-// row sees, is computed by a plain f32 loop instead. From a plain tile on, or from one that needs a smaller
+// row sees, is computed by a plain f32 loop instead (as long as 60 to 90 tiles). From a plain tile on, or from one that needs a smaller
 // power of two of V than those before, the sums are kept in a scale of their own, 2^-16, in which f32 holds
 // those of all finite values.
 #pragma once

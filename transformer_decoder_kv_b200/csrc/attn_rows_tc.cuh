@@ -291,7 +291,7 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     uint32_t bad = 0;                              // blocks of the tile at hand without a page
 
     // Looks a tile over before its K is unpacked: powers of two, blocks without a page. True when
-    // something that a row sees is not finite.
+    // something that a row sees is not finite, or its scales are too far apart.
     auto survey4 = [&](int c) {
         const int buf = (c - c0) & 1, j0 = unit_chunk(k, c) * kRtKeys;
         bad = 0;
@@ -400,8 +400,8 @@ static __global__ void __launch_bounds__(kRtThreads, 2) k_attn_rows_tc(const Row
     float4 vf[KV4 ? 1 : 8];                        // f32: the next tile's V
 
     // Gets tile c ready for its scores: looks it over, and K into sK (every thread is done with the last
-    // tile's scores), an f32 V into registers. True when something that a row sees is not finite: the
-    // tile is left to the plain loop. All threads return the same.
+    // tile's scores), an f32 V into registers. True when something that a row sees is not finite, or its
+    // keys are too far apart: the tile is left to the plain loop. All threads return the same.
     auto prepare = [&](int c, int entry) -> bool {
         fac = 1.0f;
         bool plain = false;
